@@ -82,8 +82,20 @@ typedef enum {
     AWQ_ERR_ARCH = 5,           /* the current device is not sm_100 (B200)         */
     AWQ_ERR_CUDA = 6,           /* a CUDA runtime/driver call or launch failed     */
     AWQ_ERR_DEVICE_TIMEOUT = 7, /* a bounded wait inside a kernel ran out          */
-    AWQ_ERR_WORKSPACE = 8       /* workspace NULL or smaller than required         */
+    AWQ_ERR_WORKSPACE = 8,      /* workspace NULL or smaller than required         */
+    AWQ_ERR_RANGE = 9,          /* a length, slot, page or offset in device memory lies
+                                   outside what the call was given                 */
+    AWQ_ERR_CAPACITY = 10       /* the free pages do not suffice                   */
 } awq_status_t;
+
+/* Activations of awq_w4a16_gemm_epilogue. */
+typedef enum {
+    AWQ_ACT_NONE = 0,
+    AWQ_ACT_RELU = 1,
+    AWQ_ACT_SILU = 2,           /* t / (1 + e^-t)                                  */
+    AWQ_ACT_GELU = 3,           /* t (1 + erf(t / sqrt 2)) / 2                     */
+    AWQ_ACT_GELU_TANH = 4       /* t (1 + tanh(sqrt(2/pi) (t + 0.044715 t^3))) / 2 */
+} awq_act_t;
 
 typedef void *awq_stream_t; /* a cudaStream_t */
 
@@ -341,6 +353,161 @@ AWQ_API awq_status_t awq_w4a16_gemm_noalloc(const uint16_t *X, const uint16_t *s
                                             const uint16_t *scales, const int32_t *zeros,
                                             int64_t M, int64_t K, int64_t N, uint16_t *Y,
                                             int32_t *dev_status, awq_stream_t stream);
+
+/*
+ * awq_w4a16_gemm with what follows the product fused into it, before the
+ * single rounding to binary16 ("Awq Quantization", "Layer Fusion": gate and up
+ * as one projection):
+ *   t[m, n] = sum_k (X[m, k] / s_k) dequant(Q)[k, n] + bias[n]      (float)
+ *   a       = act(t)                          Y [M, N], or, gated != 0,
+ *   a[m, j] = act(t[m, 2j]) * t[m, 2j + 1]    Y [M, N/2]: the columns of gate
+ *             and up interleaved when the weights were quantized; N % 16 == 0
+ *   Y       = binary16_RNE(a + residual)
+ *   bias      binary16 [N] or NULL
+ *   act       an awq_act_t
+ *   residual  binary16, the shape of Y, or NULL; residual == Y adds in place
+ *             (any other overlap is not allowed)
+ * X, s, Q, scales, zeros, M, K, N, the workspace, the tile paths and the device
+ * errors are those of awq_w4a16_gemm, and with no bias, activation, gate and
+ * residual so is every bit of Y.  bias is layer state like scales; residual is
+ * read only after the previous kernel on the stream has completed.
+ */
+AWQ_API awq_status_t awq_w4a16_gemm_epilogue(const uint16_t *X, const uint16_t *s, const int32_t *Q,
+                                             const uint16_t *scales, const int32_t *zeros, int64_t M,
+                                             int64_t K, int64_t N, const uint16_t *bias, int32_t act,
+                                             int32_t gated, const uint16_t *residual, uint16_t *Y,
+                                             void *workspace, size_t workspace_bytes,
+                                             int32_t *dev_status, awq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 4-bit key/value cache.
+ *
+ * The weights' 4-bit grid applied to the other tensor that fills a serving
+ * GPU: the keys and values of every token, one group per token and head.
+ * Head dimension D = 64 or 128; page_size = 16, 32, 64, 128 or 256 tokens.
+ *
+ *   cache        uint8 [num_pages, kv_heads, page_size / 16] blocks; a block is
+ *                16 tokens of one head, 16 D + 128 bytes: key codes (16 rows of
+ *                D / 2 bytes, sequential nibbles as in Q), value codes, then 16
+ *                words for the keys and 16 for the values: step (binary16) in
+ *                bits 0..15, zero point in bits 16..31
+ *   block_table  int32 [B, max_pages]: the pages of each request, in order
+ *   lens         int32 [B]: cached tokens of each request
+ *   free_pages   int32 [num_pages], free_count int32 [1]: a stack of free pages
+ *   slot         page * page_size + position in the page (int64); negative: none
+ * Lengths and tables live in device memory and are read there, so a captured
+ * graph follows them.  What they hold is checked on the device: an entry out of
+ * range is reported as AWQ_ERR_RANGE and skipped, never followed.
+ * ------------------------------------------------------------------------ */
+#define AWQ_KV4_BLOCK 16
+#define AWQ_KV4_MAX_REQUESTS 4096
+#define AWQ_KV4_MAX_HEADS 1024      /* query heads; key/value heads likewise */
+
+/* Bytes of one page for one head; 0 for an unsupported page_size or D. */
+AWQ_API size_t awq_kv4_page_bytes(int64_t page_size, int64_t D);
+
+/*
+ * Block table, slot map and positions of a step, from request lengths.
+ * Request b has lens[b] tokens in ceil(lens[b] / page_size) pages and gets
+ * new_lens[b] >= 0 more; the pages it lacks are popped from the stack, in the
+ * order of requests, then of positions, and entered in its table row.
+ *   slots      int64 [T] (output): of every new token, requests one after the
+ *              other; -1 in the rows behind the last one (T >= their number)
+ *   positions  int32 [T] (output) or NULL: position in the request; -1 there
+ *   cu         int32 [B + 1] (output): first row of each request, and their end
+ *   lens_out, free_count_out  (outputs): lengths and stack after the step; may be
+ *              lens and free_count themselves
+ *   1 <= B <= AWQ_KV4_MAX_REQUESTS, 1 <= T < 2^31, max_pages * page_size < 2^31
+ * Device errors: AWQ_ERR_RANGE (a negative length, more tokens than T, more
+ * pages than max_pages, free_count outside 0..num_pages), AWQ_ERR_CAPACITY (too few
+ * free pages).  Then nothing is reserved: slots and positions are -1, cu is 0,
+ * lengths, table and stack are unchanged.
+ */
+AWQ_API awq_status_t awq_kv4_reserve(const int32_t *new_lens, const int32_t *lens, int64_t B,
+                                     int64_t page_size, int32_t *block_table, int64_t max_pages,
+                                     const int32_t *free_pages, const int32_t *free_count,
+                                     int64_t num_pages, int64_t T, int64_t *slots, int32_t *positions,
+                                     int32_t *cu, int32_t *lens_out, int32_t *free_count_out,
+                                     int32_t *dev_status, awq_stream_t stream);
+
+/*
+ * Ends requests: the pages of every request b with done[b] != 0 are pushed onto
+ * the stack, in the order of requests, then of positions; its length becomes 0
+ * and the table entries of those pages -1.
+ *   done int32 [B]; lens, block_table, free_pages, free_count updated in place
+ * Device errors: AWQ_ERR_RANGE (a length or page out of range, more pages than
+ * num_pages in the stack); then nothing is changed.
+ */
+AWQ_API awq_status_t awq_kv4_release(const int32_t *done, int32_t *lens, int64_t B, int64_t page_size,
+                                     int32_t *block_table, int64_t max_pages, int32_t *free_pages,
+                                     int32_t *free_count, int64_t num_pages, int32_t *dev_status,
+                                     awq_stream_t stream);
+
+/*
+ * Quantizes the keys and values of T tokens into their slots.  Per token and head:
+ *   lo = min(0, min x), hi = max(0, max x)
+ *   step = binary16_RNE(max(hi - lo, 1e-5f) / 15)
+ *   z = clamp(rint(-lo / step), 0, 15)
+ *   q = clamp(rint(x * (1 / step)) + z, 0, 15)            (rint: ties to even)
+ * in IEEE float; the result is bit-exact.  The value it stands for is (q - z) step.
+ *   k, v   binary16, token t at k + t * k_stride (elements), heads of D one after
+ *          the other; strides >= kv_heads * D, multiples of 8: slices of a fused
+ *          projection's rows are taken as they are
+ *   slots  int64 [T]; a negative one stores nothing.  A slot named twice holds
+ *          one token's codes or a mix of both
+ * Device errors: AWQ_ERR_RANGE (a slot outside the cache; that token is not
+ * stored), AWQ_ERR_NONFINITE (NaN or Inf; that token's row is unspecified).
+ */
+AWQ_API awq_status_t awq_kv4_append(const uint16_t *k, int64_t k_stride, const uint16_t *v,
+                                    int64_t v_stride, const int64_t *slots, int64_t T, int64_t kv_heads,
+                                    int64_t D, uint8_t *cache, int64_t num_pages, int64_t page_size,
+                                    int32_t *dev_status, awq_stream_t stream);
+
+/*
+ * The stored keys and values of T slots: k, v binary16 [T, kv_heads, D]
+ * (outputs), (q - z) step rounded once; zeros for a negative slot.
+ * Device errors: AWQ_ERR_RANGE (a slot outside the cache; zeros).
+ */
+AWQ_API awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_heads, int64_t D,
+                                  const uint8_t *cache, int64_t num_pages, int64_t page_size,
+                                  uint16_t *k, uint16_t *v, int32_t *dev_status, awq_stream_t stream);
+
+/*
+ * Attention over the cache.  Request b owns the query rows cu[b] .. cu[b+1] - 1;
+ * its i-th query stands at position p = lens[b] - n_b + i (n_b its number of
+ * queries: the request's last tokens, already stored) and sees the cached
+ * positions j <= p, with window > 0 only those with j > p - window:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * in float, over the values the codes stand for, rounded once to binary16; a
+ * query that sees nothing gives zeros.  Query head h reads key/value head
+ * h / (q_heads / kv_heads).
+ *   q       binary16, row t at q + t * q_stride (elements, a multiple of 8,
+ *           >= q_heads * D)
+ *   cu      int32 [B + 1], or NULL: one query per request (T >= B)
+ *   max_new the most queries of one request (a bound known on the host)
+ *   out     binary16 [T, q_heads, D] (output); rows of no request are not written
+ *   workspace  at least awq_kv4_attention_workspace_size(D) bytes, no initial
+ *           contents required, overwritten; calls that can run at the same time
+ *           need separate ones
+ *   q_heads % kv_heads == 0, both <= AWQ_KV4_MAX_HEADS; 1 <= B <=
+ *   AWQ_KV4_MAX_REQUESTS; 1 <= T, max_new < 2^31; max_pages * page_size < 2^31;
+ *   B * kv_heads * ceil(max_new * q_heads / kv_heads / 8) * (max_pages * page_size /
+ *   32 + 1) < 2^32
+ * The result depends on the number of SMs (which fixes the order of sums),
+ * never on timing: the same call gives the same bits.
+ * Device errors: AWQ_ERR_RANGE (a length above max_pages * page_size or negative:
+ * clamped; a page outside the cache: its tokens are not seen; offsets outside
+ * 0..T or a request with more than max_new queries: its rows are not written),
+ * AWQ_ERR_DEVICE_TIMEOUT.
+ */
+AWQ_API size_t awq_kv4_attention_workspace_size(int64_t D);
+AWQ_API awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, int64_t q_heads,
+                                       const uint8_t *cache, int64_t num_pages, int64_t page_size,
+                                       int64_t kv_heads, int64_t D, const int32_t *block_table,
+                                       int64_t max_pages, const int32_t *lens, const int32_t *cu, int64_t B,
+                                       int64_t max_new, float scale, int64_t window, uint16_t *out,
+                                       void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                       awq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,12 @@ Functions (names follow the C ABI):
                                       smallest output error on the calibration rows
   QuantLinear(Q, scales, zeros, s)     a quantized layer ("WQLinear"): weights checked once,
                                        layer(X) -> Y with only X and Y checked per call
+  w4a16_gemm_epilogue(X, s, Q, scales, zeros, bias, act, gated, residual)
+                                       the product with bias, activation, gate and residual
+                                       before its rounding (QuantLinear takes the same)
+  interleave_gate_up(gate, up)         weight columns as a gated product wants them
+  KV4Pages, KV4Cache                   a paged key/value cache in 4 bits: pages and slots of a
+                                       step from request lengths, store, load, attention
 """
 from __future__ import annotations
 
@@ -46,9 +52,14 @@ ABI_VERSION = 5
 STATUS = {
     0: "AWQ_OK", 1: "AWQ_ERR_NULL", 2: "AWQ_ERR_SHAPE", 3: "AWQ_ERR_ALIGN",
     4: "AWQ_ERR_NONFINITE", 5: "AWQ_ERR_ARCH", 6: "AWQ_ERR_CUDA",
-    7: "AWQ_ERR_DEVICE_TIMEOUT", 8: "AWQ_ERR_WORKSPACE",
+    7: "AWQ_ERR_DEVICE_TIMEOUT", 8: "AWQ_ERR_WORKSPACE", 9: "AWQ_ERR_RANGE", 10: "AWQ_ERR_CAPACITY",
 }
 OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_NONFINITE, ERR_ARCH, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE = range(9)
+ERR_RANGE, ERR_CAPACITY = 9, 10
+
+# activations of a fused epilogue (awq_act_t)
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+KV4_MAX_REQUESTS = 4096
 
 # exported symbols, in declaration order of include/awq_b200.h
 SYMBOLS = (
@@ -60,6 +71,9 @@ SYMBOLS = (
     "awq_w4a16_gemm_workspace_size", "awq_w4a16_gemm",
     "awq_scales_alpha", "awq_scale_search_workspace_size", "awq_scale_search",
     "awq_w4a16_gemm_noalloc",
+    "awq_w4a16_gemm_epilogue",
+    "awq_kv4_page_bytes", "awq_kv4_reserve", "awq_kv4_release", "awq_kv4_append", "awq_kv4_load",
+    "awq_kv4_attention_workspace_size", "awq_kv4_attention",
 )
 NOALLOC_SCRATCH_BYTES = 24 << 20
 
@@ -104,6 +118,21 @@ def lib() -> ctypes.CDLL:
         L.awq_scale_search_workspace_size.argtypes = [I64, I64, I64]
         L.awq_scale_search_workspace_size.restype = SZ
         L.awq_scale_search.argtypes = [P, I64, I64, P, I64, P, P, P, P, SZ, P, P]
+        I32, F32 = ctypes.c_int32, ctypes.c_float
+        L.awq_w4a16_gemm_epilogue.argtypes = [P, P, P, P, P, I64, I64, I64, P, I32, I32, P, P, P, SZ, P, P]
+        L.awq_kv4_page_bytes.argtypes = [I64, I64]
+        L.awq_kv4_page_bytes.restype = SZ
+        L.awq_kv4_reserve.argtypes = [P, P, I64, I64, P, I64, P, P, I64, I64, P, P, P, P, P, P, P]
+        L.awq_kv4_release.argtypes = [P, P, I64, I64, P, I64, P, P, I64, P, P]
+        L.awq_kv4_append.argtypes = [P, I64, P, I64, P, I64, I64, I64, P, I64, I64, P, P]
+        L.awq_kv4_load.argtypes = [P, I64, I64, I64, P, I64, I64, P, P, P, P]
+        L.awq_kv4_attention_workspace_size.argtypes = [I64]
+        L.awq_kv4_attention_workspace_size.restype = SZ
+        L.awq_kv4_attention.argtypes = [P, I64, I64, I64, P, I64, I64, I64, I64, P, I64, P, P, I64, I64, F32, I64,
+                                        P, P, SZ, P, P]
+        for name in ("awq_w4a16_gemm_epilogue", "awq_kv4_reserve", "awq_kv4_release", "awq_kv4_append",
+                     "awq_kv4_load", "awq_kv4_attention"):
+            getattr(L, name).restype = ctypes.c_int
         for name in ("awq_act_stats", "awq_compute_scales", "awq_quantize_pack",
                      "awq_quantize_pack_symmetric", "awq_quantize_pack_clip", "awq_fold_inverse_scale",
                      "awq_w4a16_gemv",
@@ -442,14 +471,85 @@ def w4a16_gemv(X, s, Q, scales, zeros, status=None, out=None, workspace=None) ->
     return Y
 
 
+def _check_epilogue(N, bias, act, gated, dev):
+    """Checks the layer side of an epilogue; returns (act code, gated flag, columns of Y)."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(k for k in ACTIVATIONS if k)} or None, got {act!r}")
+    if bias is not None:
+        _need(bias, torch.float16, (N,), "bias", dev)
+    if gated and N % 16:
+        raise ValueError(f"a gated product needs N = {N} to be a multiple of 16")
+    return ACTIVATIONS[act], int(bool(gated)), N // 2 if gated else N
+
+
+def _epilogue_workspace(dev, M, K, need):
+    """Default workspace of a call: the stream's cached one.  A call that is being captured into a graph gets its
+    own (from the graph's memory, its counters zeroed by the graph), because graphs captured on one stream
+    may be replayed at the same time on others."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws[:32768].zero_()
+        return ws
+    return workspace_for(dev, need)
+
+
+def w4a16_gemm_epilogue(X, s, Q, scales, zeros, bias=None, act=None, gated=False, residual=None, status=None,
+                        out=None, workspace=None) -> torch.Tensor:
+    """Y = act((X / s) . dequant(Q) + bias) + residual, rounded once to float16.
+
+    act: None, "relu", "silu", "gelu" or "gelu_tanh".
+    gated: columns 2j are the gate of columns 2j + 1 (see interleave_gate_up): Y is
+    act(t[:, 0::2]) * t[:, 1::2] + residual, [M, N/2].
+    residual: float16 of Y's shape; out may be residual itself.
+    workspace: as for w4a16_gemm; by default the stream's cached one, or the graph's own during capture."""
+    _need(X, torch.float16, 2, "X")
+    M, K = X.shape
+    dev = X.device
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 2:
+        raise ValueError("Q must be an int32 [K/8, N] tensor")
+    N = Q.shape[1]
+    _check_weights(K, N, s, Q, scales, zeros, dev)
+    code, gate, cols = _check_epilogue(N, bias, act, gated, dev)
+    if residual is not None:
+        _need(residual, torch.float16, (M, cols), "residual", dev)
+    _need_status(status, dev)
+    if out is None:
+        Y = torch.empty(M, cols, dtype=torch.float16, device=dev)
+    else:
+        _check_out(out, M, cols, dev)
+        Y = out
+    with _on(dev):
+        wsz = gemm_workspace_size(M, K, N)
+        if workspace is None:
+            workspace = _epilogue_workspace(dev, M, K, wsz)
+        else:
+            _check_workspace(workspace, wsz, dev)
+        _check(lib().awq_w4a16_gemm_epilogue(_ptr(X), _ptr(s), _ptr(Q), _ptr(scales), _ptr(zeros), M, K, N,
+                                             _ptr(bias), code, gate, _ptr(residual), _ptr(Y), _ptr(workspace),
+                                             workspace.numel(), _ptr(status), _stream(X)),
+               "awq_w4a16_gemm_epilogue")
+    return Y
+
+
+def interleave_gate_up(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
+    """The weight [K, 2 I] of a gated product from its gate and up weights [K, I]: column 2j from the gate,
+    column 2j + 1 from up.  Quantize the result and pass gated=True.  Biases [I] interleave the same way."""
+    if gate.shape != up.shape:
+        raise ValueError(f"gate {tuple(gate.shape)} and up {tuple(up.shape)} must have one shape")
+    return torch.stack((gate, up), dim=-1).flatten(-2)
+
+
 class QuantLinear:
     """A quantized linear layer ("Awq Quantization", "WQLinear Kernel
     Variants": one module whose forward runs the fused-dequantization kernel).
 
     The weights (Q, scales, zeros, s) are checked once here; a call checks
-    only X and the output, and passes prepared pointers to the C ABI."""
+    only X and the output, and passes prepared pointers to the C ABI.
 
-    def __init__(self, Q, scales, zeros=None, s=None):
+    bias, act and gated fuse what follows the product (w4a16_gemm_epilogue);
+    a call may add a residual: layer(X, residual=r)."""
+
+    def __init__(self, Q, scales, zeros=None, s=None, bias=None, act=None, gated=False):
         if not isinstance(Q, torch.Tensor) or Q.dim() != 2:
             raise ValueError("Q must be an int32 [K/8, N] tensor")
         self.K, self.N = Q.shape[0] * 8, Q.shape[1]
@@ -457,30 +557,308 @@ class QuantLinear:
         _check_weights(self.K, self.N, s, Q, scales, zeros, self.device)
         self.Q, self.scales, self.zeros, self.s = Q, scales, zeros, s
         self._wptrs = (_ptr(s), _ptr(Q), _ptr(scales), _ptr(zeros))
+        self.bias, self.act, self.gated = bias, act, bool(gated)
+        self._act, self._gate, self.out_features = _check_epilogue(self.N, bias, act, gated, self.device)
+        self._plain = bias is None and self._act == 0 and not gated
         self._dev_index = self.device.index if self.device.index is not None else torch.cuda.current_device()
         self._lib = lib()
 
-    def __call__(self, X, out=None, status=None, workspace=None) -> torch.Tensor:
+    def __call__(self, X, out=None, status=None, workspace=None, residual=None) -> torch.Tensor:
         if not isinstance(X, torch.Tensor) or X.dtype != torch.float16 or X.dim() != 2 \
                 or X.shape[1] != self.K or X.device != self.device or not X.is_contiguous():
             raise ValueError(f"X must be a contiguous float16 [M, {self.K}] tensor on {self.device}")
         M = X.shape[0]
+        cols = self.out_features
         if out is None:
-            out = torch.empty(M, self.N, dtype=torch.float16, device=self.device)
-        elif out.dtype != torch.float16 or tuple(out.shape) != (M, self.N) or out.device != self.device \
+            out = torch.empty(M, cols, dtype=torch.float16, device=self.device)
+        elif out.dtype != torch.float16 or tuple(out.shape) != (M, cols) or out.device != self.device \
                 or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous float16 [{M}, {self.N}] tensor on {self.device}")
+            raise ValueError(f"out must be a contiguous float16 [{M}, {cols}] tensor on {self.device}")
+        if residual is not None and (
+                residual.dtype != torch.float16 or tuple(residual.shape) != (M, cols)
+                or residual.device != self.device or not residual.is_contiguous()):
+            raise ValueError(f"residual must be a contiguous float16 [{M}, {cols}] tensor on {self.device}")
         if status is not None:
             _need_status(status, self.device)
         stream = torch._C._cuda_getCurrentRawStream(self._dev_index)
         wsz = self._lib.awq_w4a16_gemm_workspace_size(M, self.K, self.N)
+        plain = self._plain and residual is None
         if workspace is None:
-            workspace = workspace_for(self.device, wsz)
+            with _on(self.device):
+                workspace = workspace_for(self.device, wsz) if plain else \
+                    _epilogue_workspace(self.device, M, self.K, wsz)
         else:
             _check_workspace(workspace, wsz, self.device)
         s, q, sc, z = self._wptrs
         with _on(self.device):
+            if not plain:
+                _check(self._lib.awq_w4a16_gemm_epilogue(
+                    X.data_ptr(), s, q, sc, z, M, self.K, self.N, _ptr(self.bias), self._act, self._gate,
+                    _ptr(residual), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status), stream),
+                    "awq_w4a16_gemm_epilogue")
+                return out
             _check(self._lib.awq_w4a16_gemm(X.data_ptr(), s, q, sc, z, M, self.K, self.N, out.data_ptr(),
                                             workspace.data_ptr(), workspace.numel(), _ptr(status), stream),
                    "awq_w4a16_gemm")
         return out
+
+
+# ---------------------------------------------------------------- paged 4-bit key/value cache
+KV4_PAGE_SIZES = (16, 32, 64, 128, 256)
+
+
+def kv4_page_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one page for one head."""
+    n = int(lib().awq_kv4_page_bytes(page_size, head_dim))
+    if n == 0:
+        raise ValueError(f"page_size must be one of {KV4_PAGE_SIZES} and head_dim 64 or 128, "
+                         f"got {page_size} and {head_dim}")
+    return n
+
+
+def _match(t, dtype, shape, name, dev):
+    """_need for the calls of a step: one test when all is well."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _need(t, dtype, shape, name, dev)
+
+
+class KV4Pages:
+    """Pages of a 4-bit key/value cache and the requests that hold them; shared by the caches of all layers.
+
+    num_pages pages of page_size tokens (16, 32, 64, 128 or 256); max_requests rows of at most max_pages
+    pages.  State on the device, all int32: block_table [max_requests, max_pages], lens [max_requests],
+    free_pages [num_pages] with free_count [1] (a stack).  Given tensors are used as they are; by default every page is
+    free."""
+
+    def __init__(self, num_pages, page_size, max_requests, max_pages, device="cuda", block_table=None, lens=None,
+                 free_pages=None, free_count=None):
+        if page_size not in KV4_PAGE_SIZES:
+            raise ValueError(f"page_size must be one of {KV4_PAGE_SIZES}, got {page_size}")
+        if not 1 <= max_requests <= KV4_MAX_REQUESTS:
+            raise ValueError(f"max_requests must be in 1..{KV4_MAX_REQUESTS}, got {max_requests}")
+        if num_pages < 1 or num_pages >= 2**31 or max_pages < 1 or max_pages * page_size >= 2**31:
+            raise ValueError(f"num_pages = {num_pages} and max_pages * page_size = {max_pages * page_size} must be "
+                             "positive and below 2**31")
+        if (free_pages is None) != (free_count is None):
+            raise ValueError("free_pages and free_count go together")
+        first = next((t for t in (block_table, lens, free_pages) if isinstance(t, torch.Tensor)), None)
+        dev = first.device if first is not None else torch.device(device)
+        if dev.type != "cuda":
+            raise TypeError(f"the pages live on a CUDA device, got {dev}")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device, self.num_pages, self.page_size = dev, num_pages, page_size
+        self.max_requests, self.max_pages = max_requests, max_pages
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.block_table = block_table if block_table is not None else \
+            torch.full((max_requests, max_pages), -1, **i32)
+        self.lens = lens if lens is not None else torch.zeros(max_requests, **i32)
+        self.free_pages = free_pages if free_pages is not None else torch.arange(num_pages - 1, -1, -1, **i32)
+        self.free_count = free_count if free_count is not None else torch.full((1,), num_pages, **i32)
+        _need(self.block_table, torch.int32, (max_requests, max_pages), "block_table", dev)
+        _need(self.lens, torch.int32, (max_requests,), "lens", dev)
+        _need(self.free_pages, torch.int32, (num_pages,), "free_pages", dev)
+        _need(self.free_count, torch.int32, (1,), "free_count", dev)
+        self._lib = lib()
+
+    def reserve(self, new_lens, total, next_lens=None, next_free=None, out=None, status=None):
+        """Pages and slots for new_lens[b] new tokens of each request b (int32 [max_requests]).
+
+        total: rows of the step, at least the sum of new_lens (the rows behind are padding).
+        Returns (slots int64 [total], positions int32 [total], cu int32 [max_requests + 1]); slots and positions are
+        -1 in the padding.  The new lengths and free count go to next_lens and next_free (default: in place).
+        status receives ERR_CAPACITY when the free pages do not suffice, ERR_RANGE for impossible lengths; then nothing
+        is reserved and every slot is -1."""
+        dev, B = self.device, self.max_requests
+        _match(new_lens, torch.int32, (B,), "new_lens", dev)
+        if not 1 <= total < 2**31:
+            raise ValueError(f"total must be in 1..2**31 - 1, got {total}")
+        if next_lens is None:
+            next_lens = self.lens
+        else:
+            _match(next_lens, torch.int32, (B,), "next_lens", dev)
+        if next_free is None:
+            next_free = self.free_count
+        else:
+            _match(next_free, torch.int32, (1,), "next_free", dev)
+        if out is None:
+            slots = torch.empty(total, dtype=torch.int64, device=dev)
+            ints = torch.empty(total + B + 1, dtype=torch.int32, device=dev)
+            positions, cu = ints[:total], ints[total:]
+        else:
+            slots, positions, cu = out
+            _match(slots, torch.int64, (total,), "slots", dev)
+            _match(positions, torch.int32, (total,), "positions", dev)
+            _match(cu, torch.int32, (B + 1,), "cu", dev)
+        if status is not None:
+            _need_status(status, dev)
+        with _on(dev):
+            _check(self._lib.awq_kv4_reserve(
+                new_lens.data_ptr(), self.lens.data_ptr(), B, self.page_size, self.block_table.data_ptr(),
+                self.max_pages, self.free_pages.data_ptr(), self.free_count.data_ptr(), self.num_pages, total,
+                slots.data_ptr(), positions.data_ptr(), cu.data_ptr(), next_lens.data_ptr(), next_free.data_ptr(),
+                _ptr(status), _raw_stream(dev)), "awq_kv4_reserve")
+        return slots, positions, cu
+
+    def release(self, done, status=None):
+        """Ends the requests with done[b] != 0 (int32 [max_requests]): their pages return to the stack."""
+        dev = self.device
+        _match(done, torch.int32, (self.max_requests,), "done", dev)
+        if status is not None:
+            _need_status(status, dev)
+        with _on(dev):
+            _check(self._lib.awq_kv4_release(
+                done.data_ptr(), self.lens.data_ptr(), self.max_requests, self.page_size,
+                self.block_table.data_ptr(), self.max_pages, self.free_pages.data_ptr(), self.free_count.data_ptr(),
+                self.num_pages, _ptr(status), _raw_stream(dev)), "awq_kv4_release")
+
+
+class KV4Cache:
+    """Keys and values of one layer in 4 bits, on the pages of a KV4Pages.
+
+    data: uint8 [num_pages, kv_heads, kv4_page_bytes(page_size, head_dim)] (default: a zeroed one)."""
+
+    def __init__(self, pages: KV4Pages, kv_heads: int, head_dim: int, data=None):
+        if not 1 <= kv_heads <= 1024:
+            raise ValueError(f"kv_heads must be in 1..1024, got {kv_heads}")
+        self.pages, self.kv_heads, self.head_dim = pages, kv_heads, head_dim
+        size = kv4_page_bytes(pages.page_size, head_dim)
+        shape = (pages.num_pages, kv_heads, size)
+        self.data = data if data is not None else torch.zeros(shape, dtype=torch.uint8, device=pages.device)
+        _need(self.data, torch.uint8, shape, "data", pages.device)
+        self._lib = lib()
+        self._workspace_size = int(self._lib.awq_kv4_attention_workspace_size(head_dim))
+
+    def _rows(self, x, name):
+        """(T, row stride) of keys or values [T, kv_heads, head_dim] or [T, kv_heads * head_dim], rows apart by any
+        multiple of 8 elements."""
+        H, D = self.kv_heads, self.head_dim
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if x.dtype is not torch.float16:
+            raise TypeError(f"{name} must be {torch.float16}, got {x.dtype}")
+        if x.device != self.pages.device:
+            raise ValueError(f"{name} is on {x.device}, expected {self.pages.device}")
+        sh, st = x.shape, x.stride()
+        if len(sh) == 3 and sh[1] == H and sh[2] == D:
+            if st[2] != 1 or (st[1] != D and H > 1):
+                raise ValueError(f"the heads of {name} must be contiguous, got strides {st}")
+        elif not (len(sh) == 2 and sh[1] == H * D and st[1] == 1):
+            raise ValueError(f"{name} must have shape (T, {H}, {D}) or (T, {H * D}) with contiguous rows, got {tuple(sh)}")
+        T = sh[0]
+        if T == 1:
+            return T, H * D
+        if st[0] < H * D or st[0] % 8:
+            raise ValueError(f"rows of {name} must be at least {H * D} elements apart, by a multiple of 8, got {st[0]}")
+        return T, st[0]
+
+    def append(self, k, v, slots, status=None):
+        """Quantizes keys and values [T, kv_heads, head_dim] (float16; rows may be slices of a fused projection's) into
+        slots (int64 [T]; negative: not stored)."""
+        T, ks = self._rows(k, "k")
+        Tv, vs = self._rows(v, "v")
+        dev = self.pages.device
+        if T != Tv:
+            raise ValueError(f"k has {T} rows, v {Tv}")
+        _match(slots, torch.int64, (T,), "slots", dev)
+        if status is not None:
+            _need_status(status, dev)
+        if T == 0:
+            return
+        with _on(dev):
+            _check(self._lib.awq_kv4_append(
+                k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, self.kv_heads, self.head_dim,
+                self.data.data_ptr(), self.pages.num_pages, self.pages.page_size, _ptr(status), _raw_stream(dev)),
+                "awq_kv4_append")
+
+    def load(self, slots, out=None, status=None):
+        """The stored keys and values of slots (int64 [T]): (k, v) float16 [T, kv_heads, head_dim]; zeros for a negative
+        slot."""
+        dev = self.pages.device
+        _match(slots, torch.int64, (slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else None,),
+               "slots", dev)
+        T = slots.shape[0]
+        shape = (T, self.kv_heads, self.head_dim)
+        if out is None:
+            k, v = torch.empty((2, *shape), dtype=torch.float16, device=dev)
+        else:
+            k, v = out
+            _match(k, torch.float16, shape, "k", dev)
+            _match(v, torch.float16, shape, "v", dev)
+        if status is not None:
+            _need_status(status, dev)
+        if T == 0:
+            return k, v
+        with _on(dev):
+            _check(self._lib.awq_kv4_load(
+                slots.data_ptr(), T, self.kv_heads, self.head_dim, self.data.data_ptr(), self.pages.num_pages,
+                self.pages.page_size, k.data_ptr(), v.data_ptr(), _ptr(status), _raw_stream(dev)), "awq_kv4_load")
+        return k, v
+
+    def attention(self, q, cu=None, max_new=1, scale=None, window=0, out=None, status=None, workspace=None):
+        """Causal attention of q [T, q_heads, head_dim] (float16; rows may be slices of a fused projection's) over the
+        cached tokens of the pages' requests, the new tokens among them (append first).
+
+        cu: int32 [max_requests + 1], the query rows of each request (from reserve); None: one query per request.
+        max_new: the most queries of one request.  scale: default head_dim ** -0.5.
+        window: positions seen, 0 for all.  Returns [T, q_heads, head_dim]; rows of no request are not written.
+        workspace: uint8 of kv4_attention_workspace_size(head_dim) bytes; by default the stream's cached one, or the
+        graph's own during capture."""
+        p = self.pages
+        dev, D = p.device, self.head_dim
+        if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != D or q.dtype is not torch.float16 \
+                or q.device != dev:
+            raise ValueError(f"q must be a float16 [T, q_heads, {D}] tensor on {dev}")
+        T, H, _ = q.shape
+        st = q.stride()
+        if st[2] != 1 or (st[1] != D and H > 1) or (T > 1 and (st[0] < H * D or st[0] % 8)):
+            raise ValueError(f"the heads of q must be contiguous and its rows a multiple of 8 elements apart, got strides {st}")
+        if H == 0 or H % self.kv_heads:
+            raise ValueError(f"q has {H} heads, not a multiple of the cache's {self.kv_heads}")
+        if cu is not None:
+            _match(cu, torch.int32, (p.max_requests + 1,), "cu", dev)
+        elif T < p.max_requests:
+            raise ValueError(f"without cu, q needs a row for each of the {p.max_requests} requests, got {T}")
+        if max_new < 1 or window < 0:
+            raise ValueError(f"max_new must be at least 1 and window at least 0, got {max_new} and {window}")
+        if out is None:
+            out = torch.empty((T, H, D), dtype=torch.float16, device=dev)
+        else:
+            _match(out, torch.float16, (T, H, D), "out", dev)
+        if status is not None:
+            _need_status(status, dev)
+        if T == 0:
+            return out
+        with _on(dev):
+            if workspace is None:
+                if torch.cuda.is_current_stream_capturing():
+                    workspace = torch.empty(self._workspace_size, dtype=torch.uint8, device=dev)
+                else:
+                    workspace = _kv4_workspace(dev, self._workspace_size)
+            else:
+                _check_workspace(workspace, self._workspace_size, dev)
+            _check(self._lib.awq_kv4_attention(
+                q.data_ptr(), st[0] if T > 1 else H * D, T, H, self.data.data_ptr(), p.num_pages, p.page_size,
+                self.kv_heads, D, p.block_table.data_ptr(), p.max_pages, p.lens.data_ptr(), _ptr(cu),
+                p.max_requests, max_new, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
+                workspace.data_ptr(), workspace.numel(), _ptr(status), _raw_stream(dev)), "awq_kv4_attention")
+        return out
+
+
+def kv4_attention_workspace_size(head_dim: int) -> int:
+    return int(lib().awq_kv4_attention_workspace_size(head_dim))
+
+
+# The attention's workspaces, one per (device, stream), apart from the matmul's:
+# they are overwritten and never need zeroes.
+_kv4_workspaces: dict = {}
+
+
+def _kv4_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
+    key = (device.index, _raw_stream(device))
+    ws = _kv4_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _kv4_workspaces[key] = ws
+    return ws

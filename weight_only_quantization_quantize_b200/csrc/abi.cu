@@ -4,10 +4,13 @@
 // one-time per-device architecture check, TMA descriptor encoding, workspace
 // accounting and the choice of tile path.  Every step of the computation runs
 // in the kernels of quantize.cu, fold.cu, gemv.cu, matmul_small.cu,
-// matmul_tcs.cu, matmul_tct.cu, matmul_tsk.cu, search.cu and clip.cu.
+// matmul_tcs.cu, matmul_tct.cu, matmul_tsk.cu, search.cu, clip.cu, kv4_pages.cu,
+// kv4_store.cu and kv4_attend.cu.
 #include <mutex>
 
 #include "awq_kernels.cuh"
+#include "epilogue.cuh"
+#include "kv4.cuh"
 
 namespace {
 
@@ -72,7 +75,8 @@ awq_status_t device_ready(int *sms)
                 awq::configure_small_m() != cudaSuccess ||
                 awq::configure_gemv() != cudaSuccess || awq::configure_quantize() != cudaSuccess ||
                 awq::configure_tcs() != cudaSuccess || awq::configure_search() != cudaSuccess ||
-                awq::configure_clip() != cudaSuccess) {
+                awq::configure_clip() != cudaSuccess || awq::configure_kv4_pages() != cudaSuccess ||
+                awq::configure_kv4_attend() != cudaSuccess) {
                 cudaGetLastError();
                 return AWQ_ERR_CUDA;
             }
@@ -179,7 +183,7 @@ size_t workspace_bytes(int64_t M, int64_t K, int64_t N)
 awq_status_t run_matmul(const uint16_t *X, const uint16_t *s, const int32_t *Q,
                         const uint16_t *scales, const int32_t *zeros, int64_t M, int64_t K,
                         int64_t N, uint16_t *Y, void *ws, size_t ws_bytes, int32_t *dev_status,
-                        awq_stream_t stream)
+                        awq_stream_t stream, const awq::Epilogue *epi = nullptr)
 {
     // zeros == NULL: symmetric weights (zero point 8); s == NULL: X holds X/s
     if (!X || !Q || !scales || !Y) return AWQ_ERR_NULL;
@@ -211,7 +215,7 @@ awq_status_t run_matmul(const uint16_t *X, const uint16_t *s, const int32_t *Q,
         if (!encode_2d(&tmQ, CU_TENSOR_MAP_DATA_TYPE_INT32, Q, N, K / 8, N * 4, 32, 16,
                        CU_TENSOR_MAP_SWIZZLE_128B))
             return AWQ_ERR_CUDA;
-        return from_cuda(awq::launch_gemv(gplan, tmQ, hX, hs, hsc, zeros, hY, m, k, n, dev_status, st));
+        return from_cuda(awq::launch_gemv(gplan, tmQ, hX, hs, hsc, zeros, hY, m, k, n, dev_status, epi, st));
     }
     // From about 24 tokens the small-batch layer needs more MMA rate than
     // mma.sync gives: tcgen05 with the dequantized weights in tensor memory as
@@ -226,7 +230,7 @@ awq_status_t run_matmul(const uint16_t *X, const uint16_t *s, const int32_t *Q,
             return AWQ_ERR_CUDA;
         e = from_cuda(awq::launch_prescale(hX, hs, m, k, Xp, st));
         if (e != AWQ_OK) return e;
-        return from_cuda(awq::launch_tcs(plan, tmX, tmQ, hsc, zeros, hY, m, k, n, dev_status, st));
+        return from_cuda(awq::launch_tcs(plan, tmX, tmQ, hsc, zeros, hY, m, k, n, dev_status, epi, st));
     }
     if (M < kPrefillMinM) {
         const awq::SmallMPlan plan = awq::plan_small_m(m, k, n, sms);
@@ -240,7 +244,7 @@ awq_status_t run_matmul(const uint16_t *X, const uint16_t *s, const int32_t *Q,
         e = from_cuda(awq::launch_prescale(hX, hs, m, k, Xp, st));
         if (e != AWQ_OK) return e;
         return from_cuda(awq::launch_small_m(plan, tmQ, tmX, hX, hs, hsc, zeros, hY, m, k, n,
-                                             dev_status, st));
+                                             dev_status, epi, st));
     }
     // One tile per CTA, or stream-K over the tiles' k stages where that grid
     // would leave SMs idle (few tiles, or a last wave that fills few SMs).
@@ -254,11 +258,11 @@ awq_status_t run_matmul(const uint16_t *X, const uint16_t *s, const int32_t *Q,
         return AWQ_ERR_CUDA;
     e = from_cuda(awq::launch_prescale(hX, hs, m, k, Xp, st));
     if (e != AWQ_OK) return e;
-    if (!sk) return from_cuda(awq::launch_tct(plan, tmX, tmQ, hsc, zeros, hY, m, k, n, dev_status, st));
+    if (!sk) return from_cuda(awq::launch_tct(plan, tmX, tmQ, hsc, zeros, hY, m, k, n, dev_status, epi, st));
     float *partials = reinterpret_cast<float *>(wsb + kCounterBytes + xp_bytes(M, K));
     uint32_t *flags = reinterpret_cast<uint32_t *>(wsb);
     return from_cuda(
-        awq::launch_tsk(skplan, tmX, tmQ, hsc, zeros, hY, m, k, n, partials, flags, dev_status, st));
+        awq::launch_tsk(skplan, tmX, tmQ, hsc, zeros, hY, m, k, n, partials, flags, dev_status, epi, st));
 }
 
 }  // namespace
@@ -302,6 +306,8 @@ const char *awq_status_string(awq_status_t status)
     case AWQ_ERR_CUDA: return "AWQ_ERR_CUDA: CUDA call or launch failed";
     case AWQ_ERR_DEVICE_TIMEOUT: return "AWQ_ERR_DEVICE_TIMEOUT: a kernel wait ran out";
     case AWQ_ERR_WORKSPACE: return "AWQ_ERR_WORKSPACE: workspace missing or too small";
+    case AWQ_ERR_RANGE: return "AWQ_ERR_RANGE: a length, slot, page or offset in device memory is out of range";
+    case AWQ_ERR_CAPACITY: return "AWQ_ERR_CAPACITY: too few free pages";
     }
     return "AWQ_ERR_UNKNOWN";
 }
@@ -552,6 +558,184 @@ awq_status_t awq_scale_search(const uint16_t *xcal, int64_t R, int64_t K, const 
     if (e == AWQ_OK) e = from_cuda(awq::launch_pick_best(losses, j_best, st));
     if (e == AWQ_OK) e = from_cuda(awq::launch_scales_alpha(m, k, 0, j_best, s_best, dev_status, st));
     return e;
+}
+
+}  // extern "C"
+
+extern "C" awq_status_t awq_w4a16_gemm_epilogue(const uint16_t *X, const uint16_t *s, const int32_t *Q,
+                                                const uint16_t *scales, const int32_t *zeros, int64_t M,
+                                                int64_t K, int64_t N, const uint16_t *bias, int32_t act,
+                                                int32_t gated, const uint16_t *residual, uint16_t *Y,
+                                                void *workspace, size_t workspace_bytes_,
+                                                int32_t *dev_status, awq_stream_t stream)
+{
+    awq_status_t e = awq::matmul_args_status(X, s, Q, scales, zeros, M, K, N, Y, dev_status);
+    if (e != AWQ_OK) return e;
+    if (act < AWQ_ACT_NONE || act > AWQ_ACT_GELU_TANH || (gated && N % 16 != 0)) return AWQ_ERR_SHAPE;
+    if ((bias && !aligned16(bias)) || (residual && !aligned16(residual))) return AWQ_ERR_ALIGN;
+    const bool plain = !bias && act == AWQ_ACT_NONE && !gated && !residual;
+    const awq::Epilogue epi{reinterpret_cast<const __half *>(bias), reinterpret_cast<const __half *>(residual), act,
+                            gated ? 1 : 0};
+    return run_matmul(X, s, Q, scales, zeros, M, K, N, Y, workspace, workspace_bytes_, dev_status, stream,
+                      plain ? nullptr : &epi);
+}
+
+namespace {
+// log2 of a supported page size, -1 otherwise
+int page_shift_of(int64_t page_size)
+{
+    for (int s = 4; s <= 8; ++s)
+        if (page_size == (1 << s)) return s;
+    return -1;
+}
+
+bool kv4_tables_ok(int64_t B, int64_t page_size, int64_t max_pages, int64_t num_pages)
+{
+    return B >= 1 && B <= AWQ_KV4_MAX_REQUESTS && page_shift_of(page_size) > 0 && max_pages >= 1 &&
+           max_pages <= INT32_MAX / page_size && num_pages >= 1 && num_pages <= INT32_MAX;
+}
+
+bool kv4_cache_ok(int64_t kv_heads, int64_t D, int64_t num_pages, int64_t page_size)
+{
+    return kv_heads >= 1 && kv_heads <= AWQ_KV4_MAX_HEADS && (D == 64 || D == 128) && num_pages >= 1 &&
+           num_pages <= INT32_MAX && page_shift_of(page_size) > 0;
+}
+
+awq::Kv4Cache kv4_cache(const uint8_t *data, int64_t kv_heads, int64_t D, int64_t num_pages, int64_t page_size)
+{
+    return awq::Kv4Cache{const_cast<uint8_t *>(data), num_pages, static_cast<int>(kv_heads), static_cast<int>(D),
+                         page_shift_of(page_size)};
+}
+
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+}  // namespace
+
+extern "C" {
+
+size_t awq_kv4_page_bytes(int64_t page_size, int64_t D)
+{
+    if (page_shift_of(page_size) < 0 || (D != 64 && D != 128)) return 0;
+    return static_cast<size_t>(page_size / awq::kKvBlock) * awq::kv4_block_bytes(static_cast<int>(D));
+}
+
+awq_status_t awq_kv4_reserve(const int32_t *new_lens, const int32_t *lens, int64_t B, int64_t page_size,
+                             int32_t *block_table, int64_t max_pages, const int32_t *free_pages,
+                             const int32_t *free_count, int64_t num_pages, int64_t T, int64_t *slots,
+                             int32_t *positions, int32_t *cu, int32_t *lens_out, int32_t *free_count_out,
+                             int32_t *dev_status, awq_stream_t stream)
+{
+    if (!new_lens || !lens || !block_table || !free_pages || !free_count || !slots || !cu || !lens_out ||
+        !free_count_out)
+        return AWQ_ERR_NULL;
+    if (!kv4_tables_ok(B, page_size, max_pages, num_pages) || T < 1 || T > INT32_MAX) return AWQ_ERR_SHAPE;
+    if (!aligned4(new_lens) || !aligned4(lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+        !aligned4(free_count) || !aligned8(slots) || (positions && !aligned4(positions)) || !aligned4(cu) ||
+        !aligned4(lens_out) || !aligned4(free_count_out) || (dev_status && !aligned4(dev_status)))
+        return AWQ_ERR_ALIGN;
+    int sms = 0;
+    awq_status_t e = device_ready(&sms);
+    if (e != AWQ_OK) return e;
+    return from_cuda(awq::launch_kv4_reserve(new_lens, lens, static_cast<int>(B), page_shift_of(page_size),
+                                             block_table, static_cast<int>(max_pages), free_pages, free_count,
+                                             num_pages, T, slots, positions, cu, lens_out, free_count_out,
+                                             dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+awq_status_t awq_kv4_release(const int32_t *done, int32_t *lens, int64_t B, int64_t page_size,
+                             int32_t *block_table, int64_t max_pages, int32_t *free_pages, int32_t *free_count,
+                             int64_t num_pages, int32_t *dev_status, awq_stream_t stream)
+{
+    if (!done || !lens || !block_table || !free_pages || !free_count) return AWQ_ERR_NULL;
+    if (!kv4_tables_ok(B, page_size, max_pages, num_pages)) return AWQ_ERR_SHAPE;
+    if (!aligned4(done) || !aligned4(lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+        !aligned4(free_count) || (dev_status && !aligned4(dev_status)))
+        return AWQ_ERR_ALIGN;
+    int sms = 0;
+    awq_status_t e = device_ready(&sms);
+    if (e != AWQ_OK) return e;
+    return from_cuda(awq::launch_kv4_release(done, lens, static_cast<int>(B), page_shift_of(page_size), block_table,
+                                             static_cast<int>(max_pages), free_pages, free_count, num_pages,
+                                             dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+awq_status_t awq_kv4_append(const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                            const int64_t *slots, int64_t T, int64_t kv_heads, int64_t D, uint8_t *cache,
+                            int64_t num_pages, int64_t page_size, int32_t *dev_status, awq_stream_t stream)
+{
+    if (!k || !v || !slots || !cache) return AWQ_ERR_NULL;
+    if (!kv4_cache_ok(kv_heads, D, num_pages, page_size) || T < 1 || T > INT32_MAX || k_stride < kv_heads * D ||
+        v_stride < kv_heads * D || k_stride > INT32_MAX || v_stride > INT32_MAX)
+        return AWQ_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || k_stride % 8 || v_stride % 8 || !aligned8(slots) || !aligned16(cache) ||
+        (dev_status && !aligned4(dev_status)))
+        return AWQ_ERR_ALIGN;
+    int sms = 0;
+    awq_status_t e = device_ready(&sms);
+    if (e != AWQ_OK) return e;
+    return from_cuda(awq::launch_kv4_append(kv4_cache(cache, kv_heads, D, num_pages, page_size),
+                                            reinterpret_cast<const __half *>(k), k_stride,
+                                            reinterpret_cast<const __half *>(v), v_stride, slots, T, dev_status,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_heads, int64_t D, const uint8_t *cache,
+                          int64_t num_pages, int64_t page_size, uint16_t *k, uint16_t *v, int32_t *dev_status,
+                          awq_stream_t stream)
+{
+    if (!slots || !cache || !k || !v) return AWQ_ERR_NULL;
+    if (!kv4_cache_ok(kv_heads, D, num_pages, page_size) || T < 1 || T > INT32_MAX) return AWQ_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || !aligned8(slots) || !aligned16(cache) || (dev_status && !aligned4(dev_status)))
+        return AWQ_ERR_ALIGN;
+    int sms = 0;
+    awq_status_t e = device_ready(&sms);
+    if (e != AWQ_OK) return e;
+    return from_cuda(awq::launch_kv4_load(kv4_cache(cache, kv_heads, D, num_pages, page_size), slots, T,
+                                          reinterpret_cast<__half *>(k), reinterpret_cast<__half *>(v), dev_status,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t awq_kv4_attention_workspace_size(int64_t D)
+{
+    return D == 64 || D == 128 ? awq::kv4_attend_workspace(static_cast<int>(D)) : 0;
+}
+
+awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, int64_t q_heads, const uint8_t *cache,
+                               int64_t num_pages, int64_t page_size, int64_t kv_heads, int64_t D,
+                               const int32_t *block_table, int64_t max_pages, const int32_t *lens, const int32_t *cu,
+                               int64_t B, int64_t max_new, float scale, int64_t window, uint16_t *out,
+                               void *workspace, size_t workspace_bytes_, int32_t *dev_status, awq_stream_t stream)
+{
+    if (!q || !cache || !block_table || !lens || !out) return AWQ_ERR_NULL;
+    if (!kv4_cache_ok(kv_heads, D, num_pages, page_size) || !kv4_tables_ok(B, page_size, max_pages, num_pages) ||
+        q_heads < 1 || q_heads > AWQ_KV4_MAX_HEADS || q_heads % kv_heads != 0 || T < 1 || T > INT32_MAX ||
+        q_stride < q_heads * D || q_stride > INT32_MAX || max_new < 1 || max_new > INT32_MAX || window < 0 ||
+        window > INT32_MAX || (!cu && T < B))
+        return AWQ_ERR_SHAPE;
+    // the run of tiles that the kernel splits is counted in 32 bits
+    const int64_t blocks = (max_new * (q_heads / kv_heads) + 7) / 8;
+    const int64_t tiles = max_pages * page_size / 32 + 1;
+    if (blocks > (int64_t(1) << 32) / (B * kv_heads) / tiles) return AWQ_ERR_SHAPE;
+    if (!aligned16(q) || q_stride % 8 || !aligned16(cache) || !aligned4(block_table) || !aligned4(lens) ||
+        (cu && !aligned4(cu)) || !aligned16(out) || (workspace && !aligned16(workspace)) ||
+        (dev_status && !aligned4(dev_status)))
+        return AWQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes_ < awq_kv4_attention_workspace_size(D)) return AWQ_ERR_WORKSPACE;
+    int sms = 0;
+    awq_status_t e = device_ready(&sms);
+    if (e != AWQ_OK) return e;
+    awq::Kv4AttendArgs a{};
+    a.cache = kv4_cache(cache, kv_heads, D, num_pages, page_size);
+    a.tab = awq::Kv4Tables{block_table, lens, cu, static_cast<int>(B), static_cast<int>(max_pages)};
+    a.q = reinterpret_cast<const __half *>(q);
+    a.q_stride = q_stride;
+    a.out = reinterpret_cast<__half *>(out);
+    a.T = T;
+    a.max_new = static_cast<int>(max_new);
+    a.q_heads = static_cast<int>(q_heads);
+    a.window = static_cast<int>(window);
+    a.scale = scale;
+    a.status = dev_status;
+    return from_cuda(awq::launch_kv4_attend(a, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -5,6 +5,8 @@
 
 namespace awq {
 
+struct Epilogue;  // epilogue.cuh; the matmul launchers take NULL for none
+
 // quantize.cu
 cudaError_t launch_act_stats(const __half *xcal, int R, int K, float *m, int32_t *status,
                              cudaStream_t st);
@@ -34,7 +36,8 @@ bool plan_gemv(int M, int K, int N, int num_sms, GemvPlan *plan);
 cudaError_t configure_gemv();
 cudaError_t launch_gemv(const GemvPlan &plan, const CUtensorMap &tmQ, const __half *X,
                         const __half *s, const __half *scales, const int32_t *zeros, __half *Y,
-                        int M, int K, int N, int32_t *status, cudaStream_t st);
+                        int M, int K, int N, int32_t *status, const Epilogue *epi,
+                       cudaStream_t st);
 
 // matmul_small.cu -- M < 64: register-fed tensor cores, TMA weight stream
 struct SmallMPlan {
@@ -53,7 +56,8 @@ cudaError_t launch_prescale(const __half *X, const __half *s, int M, int K, __ha
 cudaError_t launch_small_m(const SmallMPlan &plan, const CUtensorMap &tmQ, const CUtensorMap &tmX,
                            const __half *X, const __half *s, const __half *scales,
                            const int32_t *zeros, __half *Y, int M, int K, int N,
-                           int32_t *status, cudaStream_t st);
+                           int32_t *status, const Epilogue *epi,
+                       cudaStream_t st);
 
 // matmul_tct.cu -- M >= 64: tcgen05 with the dequantized weights in TMEM
 // (transposed tile: 128 output columns x bt tokens), one tile per CTA
@@ -66,7 +70,8 @@ TctPlan plan_tct(int M, int K, int N, int num_sms);
 cudaError_t configure_tct();
 cudaError_t launch_tct(const TctPlan &plan, const CUtensorMap &tmX, const CUtensorMap &tmQ,
                        const __half *scales, const int32_t *zeros, __half *Y, int M, int K, int N,
-                       int32_t *status, cudaStream_t st);
+                       int32_t *status, const Epilogue *epi,
+                       cudaStream_t st);
 
 // matmul_tsk.cu -- the same tile split along K by stream-K, for grids that
 // one tile per CTA would leave partly idle
@@ -87,7 +92,8 @@ cudaError_t configure_tsk();
 // left at zero by a call that completes without a device error.
 cudaError_t launch_tsk(const TskPlan &plan, const CUtensorMap &tmX, const CUtensorMap &tmQ,
                        const __half *scales, const int32_t *zeros, __half *Y, int M, int K, int N,
-                       float *partials, uint32_t *flags, int32_t *status, cudaStream_t st);
+                       float *partials, uint32_t *flags, int32_t *status, const Epilogue *epi,
+                       cudaStream_t st);
 
 // matmul_tcs.cu -- 24 <= M < 64: tcgen05 with the weights as the 128-row operand in TMEM
 struct TcsPlan {
@@ -101,7 +107,8 @@ TcsPlan plan_tcs(int M, int K, int N, int num_sms);
 cudaError_t configure_tcs();
 cudaError_t launch_tcs(const TcsPlan &plan, const CUtensorMap &tmX, const CUtensorMap &tmQ,
                        const __half *scales, const int32_t *zeros, __half *Y, int M, int K, int N,
-                       int32_t *status, cudaStream_t st);
+                       int32_t *status, const Epilogue *epi,
+                       cudaStream_t st);
 
 // search.cu -- scale search over alpha: scales of one grid point, transpose,
 // unquantized X W (tcgen05, float out), fixed-order loss, argmin

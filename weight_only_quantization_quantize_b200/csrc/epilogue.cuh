@@ -1,0 +1,160 @@
+// epilogue.cuh -- what follows a W4A16 product before its single rounding to
+// binary16: bias, activation, gate, residual.
+//
+//   t[m, n] = sum_k X'[m, k] w[k, n] + bias[n]               (float)
+//   a[m, n] = act(t[m, n])                                    or, gated,
+//   a[m, j] = act(t[m, 2j]) * t[m, 2j + 1]                    (N / 2 columns)
+//   Y       = binary16_RNE(a + residual)
+//
+// The matmul kernels are instantiated twice, with and without it: the plain
+// instantiations hold none of this code.  The accumulators are read where the
+// plain kernel rounds them, so the bias, the activation and the residual cost
+// their own bytes (2 N + 2 M N) and no further pass over Y.
+#pragma once
+
+#include "awq_common.cuh"
+
+namespace awq {
+
+struct Epilogue {
+    const __half *bias;      // [N] or NULL
+    const __half *residual;  // [M, columns of Y] or NULL; may be Y itself
+    int act;                 // awq_act_t
+    int gated;               // columns 2j are the gate of columns 2j + 1
+};
+
+// Activation in float.  The exponentials use the fast forms (a few units of
+// 2^-22 relative), far below the binary16 rounding that follows.
+__device__ __forceinline__ float epi_sigmoid_times(float t, float u)  // t * sigmoid(u)
+{
+    return __fdividef(t, 1.0f + __expf(-u));
+}
+
+__device__ __forceinline__ float epi_act(float t, int act)
+{
+    switch (act) {
+    case AWQ_ACT_RELU: return t < 0.0f ? 0.0f : t;  // NaN stays NaN
+    case AWQ_ACT_SILU: return epi_sigmoid_times(t, t);
+    case AWQ_ACT_GELU: return 0.5f * t * erfcf(-0.70710678f * t);
+    case AWQ_ACT_GELU_TANH:
+        // 0.5 t (1 + tanh(u)) = t sigmoid(2u), u = sqrt(2/pi) (t + 0.044715 t^3)
+        return epi_sigmoid_times(t, 1.59576912f * (t + 0.044715f * t * t * t));
+    default: return t;
+    }
+}
+
+__device__ __forceinline__ float epi_bias(const Epilogue &e, int n)
+{
+    return e.bias ? __half2float(e.bias[n]) : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    return __half_as_ushort(__float2half_rn(lo)) | (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(hi))) << 16);
+}
+
+__device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w))); }
+__device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16))); }
+
+// Eight consecutive columns n .. n + 7 of token `tok` (N columns before the
+// gate): finish and write them, 16 bytes, or 8 bytes when gated.
+__device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __half *Y, int tok, int n, int N)
+{
+    if (e.bias) {
+        const uint4 b = *reinterpret_cast<const uint4 *>(e.bias + n);
+        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] += half_lo(w[i]);
+            v[2 * i + 1] += half_hi(w[i]);
+        }
+    }
+    if (e.gated) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = epi_act(v[2 * i], e.act) * v[2 * i + 1];
+        const size_t at = static_cast<size_t>(tok) * (N / 2) + n / 2;
+        if (e.residual) {
+            const uint2 r = *reinterpret_cast<const uint2 *>(e.residual + at);
+            v[0] += half_lo(r.x); v[1] += half_hi(r.x); v[2] += half_lo(r.y); v[3] += half_hi(r.y);
+        }
+        *reinterpret_cast<uint2 *>(Y + at) = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = epi_act(v[i], e.act);
+    const size_t at = static_cast<size_t>(tok) * N + n;
+    if (e.residual) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(e.residual + at);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] += half_lo(w[i]);
+            v[2 * i + 1] += half_hi(w[i]);
+        }
+    }
+    *reinterpret_cast<uint4 *>(Y + at) = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]),
+                                                    pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+}
+
+// 32 tokens m0 .. m0 + 31 (those below m0 + mrem) of column n, one column per
+// lane (the accumulator layout of the tcgen05 kernels, n = n0 + lane with n0
+// even); every lane of the warp calls it, lanes with n >= N write nothing.
+// Gated: lanes 2j and 2j + 1 hold a gate and its column; the even lane
+// finishes the even tokens and the odd lane the odd ones, one exchange per
+// token pair.  The residual is read before the first store: Y may be the
+// residual's own memory.
+__device__ __forceinline__ void epi_store_column32(const Epilogue &e, float (&v)[32], __half *Y, int m0, int mrem,
+                                                   int n, int N)
+{
+    const bool in = n < N;
+    const float b = in ? epi_bias(e, n) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] += b;
+    if (e.gated) {
+        const bool odd = n & 1;
+        const int cols = N / 2;
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float x = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+            o[i] = odd ? epi_act(x, e.act) * v[2 * i + 1] : epi_act(v[2 * i], e.act) * x;
+        }
+        if (!in) return;
+        const int first = odd ? 1 : 0;
+        const size_t at = static_cast<size_t>(m0 + first) * cols + n / 2;
+        const size_t step = 2 * static_cast<size_t>(cols);
+        if (e.residual) {
+            const __half *r = e.residual + at;
+            __half rv[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                rv[i] = 2 * i + first < mrem ? r[i * step] : __half(__ushort_as_half(0));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] += __half2float(rv[i]);
+        }
+        __half *dst = Y + at;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (2 * i + first < mrem) dst[i * step] = __float2half_rn(o[i]);
+        return;
+    }
+    if (!in) return;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = epi_act(v[i], e.act);
+    const size_t at = static_cast<size_t>(m0) * N + n;
+    if (e.residual) {
+        const __half *r = e.residual + at;
+        __half rv[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            rv[i] = i < mrem ? r[static_cast<size_t>(i) * N] : __half(__ushort_as_half(0));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __half2float(rv[i]);
+    }
+    __half *dst = Y + at;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < mrem) dst[static_cast<size_t>(i) * N] = __float2half_rn(v[i]);
+}
+
+}  // namespace awq

@@ -36,6 +36,7 @@
 //                   transaction bytes on the owner's mbarrier); owners sum the
 //                   K-split partials locally in fixed rank order and write Y.
 #include "awq_kernels.cuh"
+#include "epilogue.cuh"
 
 namespace awq {
 
@@ -65,6 +66,7 @@ struct GemvParams {
     uint32_t mask_lo;  // 0x000F000F: nibbles 0 and 4 (after >> 8: 2 and 6)
     uint32_t mask_hi;  // 0x00F000F0: nibbles 1 and 5 (after >> 8: 3 and 7)
     uint32_t magic;    // 0x64006400: binary16 1024.0 in both halves
+    Epilogue epi;      // read by the instantiations with an epilogue only
 };
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
@@ -73,7 +75,7 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
     return p + ((1024u - (a & 1023u)) & 1023u);
 }
 
-template <int S, int MT>
+template <int S, int MT, bool EPI>
 __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
     gemv_kernel(const __grid_constant__ CUtensorMap tmQ, const GemvParams p)
 {
@@ -435,6 +437,7 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
         // the partials pushed into this CTA still land before it exits
         mbar_wait_for(recv_bar, 0, kDrainLimitNs);
     }
+    if constexpr (EPI) pdl_wait();  // every thread may read the residual
     const int lchunks = cpo / 8;
     for (int e = threadIdx.x; e < p.M * lchunks; e += kAllThreads) {
         const int tok = e / lchunks;
@@ -450,6 +453,10 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
             v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
             v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
         }
+        if constexpr (EPI) {
+            epi_store8(p.epi, v, p.Y, tok, n, p.N);
+            continue;
+        }
         uint4 o;
         o.x = __half_as_ushort(__float2half_rn(v[0])) | (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(v[1]))) << 16);
         o.y = __half_as_ushort(__float2half_rn(v[2])) | (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(v[3]))) << 16);
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
     cluster_wait_acquire();
 }
 
-template <int S, int MT>
+template <int S, int MT, bool EPI>
 cudaError_t launch_gemv_one(const GemvPlan &plan, const CUtensorMap &tmQ, const GemvParams &prm,
                             cudaStream_t st)
 {
@@ -478,14 +485,23 @@ cudaError_t launch_gemv_one(const GemvPlan &plan, const CUtensorMap &tmQ, const 
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, gemv_kernel<S, MT>, tmQ, prm);
+    return cudaLaunchKernelEx(&cfg, gemv_kernel<S, MT, EPI>, tmQ, prm);
 }
 
 template <int S, int MT>
 cudaError_t configure_gemv_one()
 {
-    return cudaFuncSetAttribute(gemv_kernel<S, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSmemOptIn);
+    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<S, MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmemOptIn);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(gemv_kernel<S, MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOptIn);
+}
+
+template <int S, int MT>
+cudaError_t launch_gemv_either(const GemvPlan &plan, const CUtensorMap &tmQ, const GemvParams &prm, bool epi,
+                               cudaStream_t st)
+{
+    return epi ? launch_gemv_one<S, MT, true>(plan, tmQ, prm, st) : launch_gemv_one<S, MT, false>(plan, tmQ, prm, st);
 }
 
 }  // namespace
@@ -548,9 +564,11 @@ bool plan_gemv(int M, int K, int N, int num_sms, GemvPlan *pl)
 
 cudaError_t launch_gemv(const GemvPlan &plan, const CUtensorMap &tmQ, const __half *X,
                         const __half *s, const __half *scales, const int32_t *zeros, __half *Y,
-                        int M, int K, int N, int32_t *status, cudaStream_t st)
+                        int M, int K, int N, int32_t *status, const Epilogue *epi, cudaStream_t st)
 {
     GemvParams prm{};
+    if (epi) prm.epi = *epi;
+    const bool e = epi != nullptr;
     prm.X = X;
     prm.s = s;
     prm.scales = scales;
@@ -570,10 +588,10 @@ cudaError_t launch_gemv(const GemvPlan &plan, const CUtensorMap &tmQ, const __ha
     prm.mask_hi = 0x00F000F0u;
     prm.magic = 0x64006400u;
     if (plan.stages == 6)
-        return M == 2 ? launch_gemv_one<6, 2>(plan, tmQ, prm, st) : launch_gemv_one<6, 1>(plan, tmQ, prm, st);
+        return M == 2 ? launch_gemv_either<6, 2>(plan, tmQ, prm, e, st) : launch_gemv_either<6, 1>(plan, tmQ, prm, e, st);
     if (plan.stages == 4)
-        return M == 2 ? launch_gemv_one<4, 2>(plan, tmQ, prm, st) : launch_gemv_one<4, 1>(plan, tmQ, prm, st);
-    return M == 2 ? launch_gemv_one<8, 2>(plan, tmQ, prm, st) : launch_gemv_one<8, 1>(plan, tmQ, prm, st);
+        return M == 2 ? launch_gemv_either<4, 2>(plan, tmQ, prm, e, st) : launch_gemv_either<4, 1>(plan, tmQ, prm, e, st);
+    return M == 2 ? launch_gemv_either<8, 2>(plan, tmQ, prm, e, st) : launch_gemv_either<8, 1>(plan, tmQ, prm, e, st);
 }
 
 }  // namespace awq

@@ -1,0 +1,802 @@
+// kv4_attend.cu -- attention over the paged 4-bit key/value cache for few query
+// rows per key/value head (single tokens and short runs of tokens): the
+// HBM-bound regime, every cached code read once.
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - max_j)
+//   k_j = step_j (c_j - z_j), and v_j likewise, so with the integer codes c
+//   q_i . k_j   = step_j (q_i . c_j - z_j sum(q_i))
+//   sum_j p v_j = sum_j (p_ij step_j) c_j - sum_j (p_ij step_j) z_j
+// Neither steps nor zero points enter the products: the tensor cores
+// (mma.sync m16n8k16, tokens or channels as rows, query rows as the 8 columns)
+// take the codes as they are packed.  A masked nibble 0x000F of a packed word
+// is the binary16 subnormal c 2^-24, and 0x00F0 is 16 c 2^-24, both exact, so
+// the unpack is one AND per pair of codes; the powers of two leave with the
+// accumulators.  A value needs the same channel of two tokens in one register:
+// one byte permute per pair of words gives that.
+//
+// Roundings: p_ij step_j to binary16 for the second product (the row sum uses
+// the unrounded float p, the zero-point sum the rounded one, so that codes and
+// zero points cancel exactly), and the output.  The reference of the
+// exponentials is kept on s + log2(step of v), and 2^8 above the largest
+// weight, so that the weights neither overflow (below 2^14 between two
+// updates) nor lose bits to subnormals within 2^-22 of the largest one.
+//
+// Work split: the (request, row block, head) items of all requests form one
+// line of 32-token tiles, and every CTA takes an equal run of it, whatever the
+// lengths.  Runs that cut an item leave (max, sum, numerator) in the workspace
+// and a second kernel joins them in a fixed order: no atomics, no waiting
+// between CTAs, the same bits every time.
+//
+// A CTA is four independent warps with a ring of kStages tiles each, filled by
+// bulk copies that the warp's first lane issues: a block of 16 tokens (keys,
+// values, steps, zero points) is one contiguous piece of the page.
+#include "awq_kernels.cuh"
+#include "kv4.cuh"
+
+namespace awq {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 32;       // tokens per ring stage: two blocks
+constexpr int kMaxCtas = 640;
+constexpr int kMinTiles = 4;    // tiles per CTA at least, one per warp
+constexpr float kGain = 8.0f;   // log2 of the largest weight after an update
+constexpr float kSlack = 13.0f; // log2 of the weight that forces an update
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D, int NT>
+struct Cfg {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kStages = 3;
+    static constexpr int kBlock = kv4_block_bytes(D);
+    static constexpr int kStage = 2 * kBlock;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kMerge = 4 * 32 * (NT * (D / 16) * 4 + 4 * NT);  // floats of one warp
+    static constexpr int kBars = 8 * kWarps * kStages;
+    static constexpr size_t kSmem = 128 + kRing + kMerge + kBars + 4 * kWarps * kStages + 64;
+    static constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
+};
+
+struct Desc {
+    int count, b, item, pad;  // CTAs that hold a part of the item this CTA begins; 0: none
+};
+
+struct Params {
+    Kv4AttendArgs a;
+    Desc *desc;      // [grid]
+    float2 *ml;      // [2 grid][rows]: (reference, sum) of a part
+    float *part;     // [2 grid][rows][D]
+    int group;
+};
+
+struct Request {
+    int len, nq, q0;   // cached tokens, queries, first query row
+    int tile0, tiles;  // first tile that any query reads, tiles from there
+    int items;         // row blocks times heads
+};
+
+template <int ROWS>
+__device__ __forceinline__ Request request_at(const Params &p, int b)
+{
+    const Kv4AttendArgs &a = p.a;
+    Request r;
+    const long long most = static_cast<long long>(a.tab.max_pages) << a.cache.page_shift;
+    r.len = a.tab.lens[b];
+    r.q0 = a.tab.cu ? a.tab.cu[b] : b;
+    const long long q1 = a.tab.cu ? a.tab.cu[b + 1] : b + 1;
+    bool bad = false;
+    if (r.len < 0 || r.len > most) {
+        bad = true;
+        r.len = r.len < 0 ? 0 : static_cast<int>(most);
+    }
+    long long nq = q1 - r.q0;
+    if (r.q0 < 0 || nq < 0 || q1 > a.T || nq > a.max_new) {
+        bad = true;
+        nq = 0;
+    }
+    if (bad) report(a.status, AWQ_ERR_RANGE);
+    r.nq = static_cast<int>(nq);
+    const long long first = a.window > 0 ? static_cast<long long>(r.len) - r.nq - a.window + 1 : 0;
+    r.tile0 = first > 0 ? static_cast<int>(first) / kTile : 0;
+    const int t = (r.len + kTile - 1) / kTile - r.tile0;
+    r.tiles = t < 1 ? 1 : t;  // rows that see nothing are still written
+    r.items = (r.nq * p.group + ROWS - 1) / ROWS * a.cache.heads;
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+template <int W>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[W])
+{
+    if constexpr (W == 4)
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+    else if constexpr (W == 2)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+    else
+        w[0] = lds32(a);
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
+
+// (step, zero point) word of a token
+__device__ __forceinline__ float meta_step(uint32_t m) { return __half2float(__ushort_as_half(static_cast<uint16_t>(m))); }
+__device__ __forceinline__ float meta_zero(uint32_t m) { return __uint_as_float(0x4B000000u | (m >> 16)) - 8388608.0f; }
+// floor(log2(step)), and -14 for subnormal steps: step < 2^(this + 1)
+__device__ __forceinline__ float meta_exp(uint32_t m)
+{
+    const int e = (m >> 10) & 31;
+    return static_cast<float>((e < 1 ? 1 : e) - 15);
+}
+
+// The block row that row r (0..7) of the first product stands for.  The second
+// product reads rows 2 t and 2 t + 1 for t = 0..3 together: this order puts
+// two even and two odd rows in each set, which halves the bank conflicts of
+// rows 64 bytes long, and keeps rows 2 i and 2 i + 1 of opposite parity.
+__device__ __forceinline__ int token_of(int r) { return r ^ ((r >> 1) & 1); }
+
+template <int D, int NT>
+struct Warp {
+    float o[NT][D / 16][4];     // numerators: [column tile][MMA][row/column]
+    float m[NT][2], l[NT][2], zs[NT][2];
+    uint32_t q[NT][D / 32][2][2];  // the second operand of the first product
+    float sumq[NT][2];
+    int hi[NT][2], lo[NT][2];   // keys lo < j <= hi of the lane's two rows
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void start_item(Warp<D, NT> &w, const Params &p, const Request &r, int item, int lane)
+{
+    constexpr int ROWS = 8 * NT;
+    const int gid = lane >> 2, t = lane & 3;
+    const int rb = item / p.a.cache.heads, head = item - rb * p.a.cache.heads;
+    const int rows = r.nq * p.group;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w.o[n][i][c] = 0.0f;
+        const int row = rb * ROWS + 8 * n + gid;
+        const bool in = row < rows;
+        const int i = in ? row / p.group : 0;
+        const __half *src = p.a.q + (r.q0 + i) * p.a.q_stride +
+                            static_cast<int64_t>(head * p.group + (in ? row - i * p.group : 0)) * D + 8 * (D / 32) * t;
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * k)) : make_uint4(0, 0, 0, 0);
+            // channels (0,4), (2,6) against the low nibbles, (1,5), (3,7) against the high ones
+            w.q[n][k][0][0] = __byte_perm(x.x, x.z, 0x5410);
+            w.q[n][k][0][1] = __byte_perm(x.y, x.w, 0x5410);
+            w.q[n][k][1][0] = __byte_perm(x.x, x.z, 0x7632);
+            w.q[n][k][1][1] = __byte_perm(x.y, x.w, 0x7632);
+            const float2 f0 = unpack2(x.x), f1 = unpack2(x.y), f2 = unpack2(x.z), f3 = unpack2(x.w);
+            sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            w.sumq[n][c] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + c));
+            w.m[n][c] = -INFINITY;
+            w.l[n][c] = w.zs[n][c] = 0.0f;
+            const int own = rb * ROWS + 8 * n + 2 * t + c;
+            const int pos = max(r.len - r.nq + own / p.group, -1);  // -1: before the first token
+            w.hi[n][c] = own < rows ? pos : -1;
+            w.lo[n][c] = p.a.window > 0 ? pos - p.a.window : -1;
+        }
+    }
+}
+
+// One tile of 32 tokens tok .. tok + 31.  full: every token is seen by every
+// row; otherwise rows are masked and blocks whose bit in `have` is clear hold
+// nothing.
+template <int D, int NT>
+__device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int tok, bool full, int have, float c1, int lane)
+{
+    constexpr int KW = D / 32;  // key words per lane and row
+    constexpr int VW = D / 64;  // value words per lane and token
+    constexpr int RB = D / 2;   // bytes of a row
+    const int gid = lane >> 2, t = lane & 3;
+    const int ra = token_of(gid);
+    float s[2][NT][4];
+    uint32_t vm[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const uint32_t base = stage + b * kv4_block_bytes(D);
+        uint32_t ka[KW], kb[KW];
+        lds_words<KW>(base + ra * RB + t * (4 * KW), ka);
+        lds_words<KW>(base + (ra + 8) * RB + t * (4 * KW), kb);
+        const uint32_t ma = lds32(base + 16 * D + 4 * ra), mb = lds32(base + 16 * D + 4 * (ra + 8));
+        vm[b][0] = lds32(base + 16 * D + 64 + 4 * ra);
+        vm[b][1] = lds32(base + 16 * D + 64 + 4 * (ra + 8));
+        float al[NT][4], ah[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) al[n][c] = ah[n][c] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+            const uint32_t a8 = ka[k] >> 8, b8 = kb[k] >> 8;
+            const uint32_t lo[4] = {ka[k] & 0x000F000Fu, kb[k] & 0x000F000Fu, a8 & 0x000F000Fu, b8 & 0x000F000Fu};
+            const uint32_t hi[4] = {ka[k] & 0x00F000F0u, kb[k] & 0x00F000F0u, a8 & 0x00F000F0u, b8 & 0x00F000F0u};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_16816(al[n], lo, w.q[n][k][0][0], w.q[n][k][0][1]);
+                mma_16816(ah[n], hi, w.q[n][k][1][0], w.q[n][k][1][1]);
+            }
+        }
+        const float fa = meta_step(ma) * c1, fb = meta_step(mb) * c1;
+        const float za = fa * meta_zero(ma) * 0x1p-24f, zb = fb * meta_zero(mb) * 0x1p-24f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                s[b][n][c] = fmaf(fa, al[n][c], fmaf(fa * 0.0625f, ah[n][c], -za * w.sumq[n][c]));
+                s[b][n][2 + c] = fmaf(fb, al[n][2 + c], fmaf(fb * 0.0625f, ah[n][2 + c], -zb * w.sumq[n][c]));
+            }
+    }
+    if (!full) {
+        // select, never multiply: what a masked place holds may be anything
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int ja = tok + 16 * b + ra;
+            const bool there = (have >> b) & 1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (!(there && ja <= w.hi[n][c] && ja > w.lo[n][c])) s[b][n][c] = -INFINITY;
+                    if (!(there && ja + 8 <= w.hi[n][c] && ja + 8 > w.lo[n][c])) s[b][n][2 + c] = -INFINITY;
+                }
+        }
+    }
+    float ev[2][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) ev[b][h] = meta_exp(vm[b][h]);
+    // the largest weight of the lane's rows; the reference moves only when one
+    // would pass 2^kSlack (one vote per tile instead of three exchanges per row)
+    float top[NT][2];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            top[n][c] = fmaxf(fmaxf(s[0][n][c] + ev[0][0], s[0][n][2 + c] + ev[0][1]),
+                              fmaxf(s[1][n][c] + ev[1][0], s[1][n][2 + c] + ev[1][1]));
+            over |= top[n][c] > w.m[n][c] + kSlack;
+        }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = top[n][c];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                if (x > w.m[n][c] + kSlack) {
+                    const float next = x - kGain;
+                    const float f = ex2(w.m[n][c] - next);  // 0 for the first one
+                    w.m[n][c] = next;
+                    w.l[n][c] *= f;
+                    w.zs[n][c] *= f;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        w.o[n][i][c] *= f;
+                        w.o[n][i][2 + c] *= f;
+                    }
+                }
+            }
+    }
+    uint32_t pb[2][NT][2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float step = meta_step(vm[b][h]), zero = meta_zero(vm[b][h]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float pv[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float x = s[b][n][2 * h + c];
+                    const float e = ex2(x - (w.m[n][c] == -INFINITY ? 0.0f : w.m[n][c]));
+                    w.l[n][c] += e;
+                    pv[c] = full || x != -INFINITY ? e * step : 0.0f;
+                }
+                const uint32_t pk = pack2(pv[0], pv[1]);
+                const float2 pr = unpack2(pk);
+                w.zs[n][0] = fmaf(pr.x, zero, w.zs[n][0]);
+                w.zs[n][1] = fmaf(pr.y, zero, w.zs[n][1]);
+                pb[b][n][h] = transpose8x8(pk);
+            }
+        }
+    const int t0 = token_of(2 * t), t1 = token_of(2 * t + 1);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const uint32_t base = stage + b * kv4_block_bytes(D) + 8 * D + gid * (4 * VW);
+        uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
+        lds_words<VW>(base + t0 * RB, v0);
+        lds_words<VW>(base + t1 * RB, v1);
+        lds_words<VW>(base + (t0 + 8) * RB, v2);
+        lds_words<VW>(base + (t1 + 8) * RB, v3);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+            const uint32_t u[4] = {__byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
+                                   __byte_perm(v2[i], v3[i], 0x5410), __byte_perm(v2[i], v3[i], 0x7632)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t mask = (j & 1) ? 0x00F000F0u : 0x000F000Fu;
+                const int sh = (j & 2) ? 8 : 0;
+                const uint32_t a[4] = {(u[0] >> sh) & mask, (u[1] >> sh) & mask, (u[2] >> sh) & mask, (u[3] >> sh) & mask};
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_16816(w.o[n][4 * i + j], a, pb[b][n][0], pb[b][n][1]);
+            }
+        }
+    }
+}
+
+// Joins another part of the same rows into (m, l, o).
+__device__ __forceinline__ void join_weights(float &m, float m2, float &f, float &f2)
+{
+    const float top = fmaxf(m, m2);
+    f = m == -INFINITY ? 0.0f : ex2(m - top);
+    f2 = m2 == -INFINITY ? 0.0f : ex2(m2 - top);
+    m = top;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kernel(const Params p)
+{
+    using C = Cfg<D, NT>;
+    extern __shared__ uint8_t smem_dyn[];
+    __shared__ uint32_t s_sum[kWarps];
+    __shared__ int s_b, s_rem;
+    const uint32_t raw = smem_u32(smem_dyn);
+    uint8_t *smem = smem_dyn + ((128u - (raw & 127u)) & 127u);
+    float *merge = reinterpret_cast<float *>(smem + C::kRing);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::kRing + C::kMerge);
+    int *haves = reinterpret_cast<int *>(smem + C::kRing + C::kMerge + C::kBars);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = static_cast<int>(blockIdx.x);
+    const Kv4AttendArgs &a = p.a;
+    const int heads = a.cache.heads;
+    pdl_launch_dependents();
+
+    // ---------------------------------------------------------------- this CTA's run of tiles
+    if (threadIdx.x < kWarps * C::kStages) mbar_init(&bars[threadIdx.x], 1);
+    fence_barrier_init();
+    const int per = (a.tab.B + kThreads - 1) / kThreads;
+    const int bfirst = static_cast<int>(threadIdx.x) * per;
+    uint32_t mine = 0;
+    for (int j = 0; j < per && bfirst + j < a.tab.B; ++j) {
+        const Request r = request_at<C::kRows>(p, bfirst + j);
+        mine += static_cast<uint32_t>(r.items) * r.tiles;
+    }
+    uint32_t pre = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, pre, d);
+        if (lane >= d) pre += y;
+    }
+    if (lane == 31) s_sum[warp] = pre;
+    __syncthreads();
+    uint32_t U = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) pre += s_sum[i];
+        U += s_sum[i];
+    }
+    pre -= mine;
+    uint32_t G = U / kMinTiles;
+    G = G < 1 ? 1 : G > gridDim.x ? gridDim.x : G;
+    const uint32_t share = U / G, rest = U % G;
+    auto begin_of = [&](uint32_t c) { return c * share + (c < rest ? c : rest); };
+    const uint32_t c = static_cast<uint32_t>(cta);
+    const uint32_t u0 = c < G ? begin_of(c) : U, u1 = c < G ? begin_of(c + 1) : U;
+    if (u0 >= u1) {
+        if (threadIdx.x == 0) p.desc[cta].count = 0;
+        return;
+    }
+    if (u0 >= pre && u0 < pre + mine) {
+        uint32_t rem = u0 - pre;
+        int b = bfirst;
+        for (; b + 1 < a.tab.B; ++b) {
+            const Request r = request_at<C::kRows>(p, b);
+            const uint32_t n = static_cast<uint32_t>(r.items) * r.tiles;
+            if (rem < n) break;
+            rem -= n;
+        }
+        s_b = b;
+        s_rem = static_cast<int>(rem);
+    }
+    __syncthreads();
+
+    // ---------------------------------------------------------------- the warp's loads
+    const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
+    uint64_t *bar = bars + warp * C::kStages;
+    int *have_of = haves + warp * C::kStages;
+    // load cursor: request, item, first tile of the segment (within the item),
+    // the segment's tiles, the next one for this warp
+    int lb = s_b;
+    Request lr = request_at<C::kRows>(p, lb);
+    int litem = static_cast<int>(static_cast<uint32_t>(s_rem) / lr.tiles);
+    int lt0 = s_rem - litem * lr.tiles;
+    uint32_t lu = u0;
+    int lseg = static_cast<int>(min(static_cast<uint32_t>(lr.tiles - lt0), u1 - u0));
+    int lnext = warp;
+    int pg0 = 0, pg1 = 0, pbatch = -1;  // pages of 32 of the warp's tiles, one per lane
+    int issued = 0;
+
+    auto issue = [&]() {
+        while (lnext >= lseg) {  // on to the next segment
+            lu += lseg;
+            if (lu >= u1) {
+                lseg = lnext = 0;
+                return;
+            }
+            lt0 = 0;
+            if (++litem >= lr.items && lb + 1 < a.tab.B) {
+                litem = 0;
+                do lr = request_at<C::kRows>(p, ++lb);
+                while (lr.items == 0 && lb + 1 < a.tab.B);
+            }
+            lseg = static_cast<int>(min(static_cast<uint32_t>(lr.tiles), u1 - lu));
+            lnext = warp;
+            pbatch = -1;
+        }
+        const int k = lnext / kWarps;  // the warp's k-th tile of the segment
+        if ((k >> 5) != pbatch) {
+            pbatch = k >> 5;
+            const int tl = warp + kWarps * (32 * pbatch + lane);
+            const int tok = (lr.tile0 + lt0 + tl) * kTile;
+            const int32_t *row = a.tab.block_table + static_cast<size_t>(lb) * a.tab.max_pages;
+            pg0 = pg1 = -1;
+            if (tl < lseg && tok < lr.len) {
+                pg0 = row[tok >> a.cache.page_shift];
+                bool bad = pg0 < 0 || pg0 >= a.cache.num_pages;
+                if (tok + kKvBlock < lr.len) {
+                    pg1 = a.cache.page_shift > 4 ? pg0 : row[(tok >> 4) + 1];
+                    bad |= pg1 < 0 || pg1 >= a.cache.num_pages;
+                    if (pg1 >= a.cache.num_pages) pg1 = -1;
+                }
+                if (pg0 >= a.cache.num_pages) pg0 = -1;
+                if (bad) report(a.status, AWQ_ERR_RANGE);
+            }
+        }
+        const int g0 = __shfl_sync(0xffffffffu, pg0, k & 31), g1 = __shfl_sync(0xffffffffu, pg1, k & 31);
+        if (lane == 0) {
+            const int tok = (lr.tile0 + lt0 + lnext) * kTile;
+            const int head = litem % heads;
+            const int st = issued % C::kStages;
+            const uint32_t dst = ring + st * C::kStage, mb = smem_u32(&bar[st]);
+            const int sh = a.cache.page_shift - 4;
+            const int64_t at = (tok >> 4) & ((1 << sh) - 1);
+            const int n0 = g0 >= 0, n1 = g1 >= 0;
+            mbar_arrive_expect_tx(&bar[st], static_cast<uint32_t>(n0 + n1) * C::kBlock);
+            const uint8_t *s0 = a.cache.data + (((static_cast<int64_t>(g0) * heads + head) << sh) + at) * C::kBlock;
+            if (n0) bulk_load(dst, s0, n1 && sh > 0 ? 2 * C::kBlock : C::kBlock, mb);
+            if (n1 && !(n0 && sh > 0)) {
+                const uint8_t *s1 =
+                    a.cache.data + (((static_cast<int64_t>(g1) * heads + head) << sh) + (sh > 0 ? at + 1 : 0)) * C::kBlock;
+                bulk_load(dst + C::kBlock, s1, C::kBlock, mb);
+            }
+            have_of[st] = n0 | (n1 << 1);
+        }
+        ++issued;
+        lnext += kWarps;
+    };
+    for (int i = 0; i < C::kStages; ++i) issue();
+    __syncwarp();
+
+    // ---------------------------------------------------------------- segments
+    int b = s_b;
+    Request r = request_at<C::kRows>(p, b);
+    int item = static_cast<int>(static_cast<uint32_t>(s_rem) / r.tiles);
+    int t0 = s_rem - item * r.tiles;
+    uint32_t u = u0;
+    int used = 0;
+    bool dead = false;
+    bool split_tail = false;
+    const float c1 = a.scale * kLog2e * 0x1p24f;
+    Warp<D, NT> w;
+    while (u < u1) {
+        const int seg = static_cast<int>(min(static_cast<uint32_t>(r.tiles - t0), u1 - u));
+        if (warp < seg) {
+            start_item<D, NT>(w, p, r, item, lane);
+            const int rb = item / heads;
+            const int ifirst = rb * C::kRows / p.group;
+            const int ilast = min((rb * C::kRows + C::kRows - 1) / p.group, r.nq - 1);
+            const int pfirst = r.len - r.nq + ifirst;                       // the earliest row's position
+            const int wlast = a.window > 0 ? max(r.len - r.nq + ilast, -1) - a.window : -1;
+            for (int k = warp; k < seg; k += kWarps) {
+                const int st = used % C::kStages;
+                if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar[st], (used / C::kStages) & 1))) {
+                    dead = true;
+                    if (lane == 0) report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+                }
+                const int have = have_of[st];
+                const int tok = (r.tile0 + t0 + k) * kTile;
+                const bool full = have == 3 && tok + kTile - 1 <= pfirst && tok > wlast;
+                if (full)
+                    tile_step<D, NT>(w, ring + st * C::kStage, tok, true, 3, c1, lane);
+                else
+                    tile_step<D, NT>(w, ring + st * C::kStage, tok, false, have, c1, lane);
+                ++used;
+                __syncwarp();
+                if (!dead) issue();
+                __syncwarp();
+            }
+            // the lanes' sums over tokens
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) {
+                        w.l[n][cc] += __shfl_xor_sync(0xffffffffu, w.l[n][cc], d);
+                        w.zs[n][cc] += __shfl_xor_sync(0xffffffffu, w.zs[n][cc], d);
+                    }
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            w.o[n][i][2 * h + cc] = w.o[n][i][2 * h + cc] * ((i & 1) ? 0x1p20f : 0x1p24f) - w.zs[n][cc];
+                }
+        }
+        // the warps' parts, last warp first, into the first warp
+        const int parts = seg < kWarps ? seg : kWarps;
+        for (int src = parts - 1; src >= 0; --src) {
+            if (warp == src) {
+                if (src < parts - 1) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int cc = 0; cc < 2; ++cc) {
+                            const float m2 = merge[(4 * n + 2 * cc) * 32 + lane], l2 = merge[(4 * n + 2 * cc + 1) * 32 + lane];
+                            float f, f2;
+                            join_weights(w.m[n][cc], m2, f, f2);
+                            w.l[n][cc] = w.l[n][cc] * f + l2 * f2;
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const float o2 = merge[(4 * NT + (n * (D / 16) + i) * 4 + 2 * h + cc) * 32 + lane];
+                                    w.o[n][i][2 * h + cc] = w.o[n][i][2 * h + cc] * f + o2 * f2;
+                                }
+                        }
+                }
+                if (src > 0) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int cc = 0; cc < 2; ++cc) {
+                            merge[(4 * n + 2 * cc) * 32 + lane] = w.m[n][cc];
+                            merge[(4 * n + 2 * cc + 1) * 32 + lane] = w.l[n][cc];
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    merge[(4 * NT + (n * (D / 16) + i) * 4 + 2 * h + cc) * 32 + lane] = w.o[n][i][2 * h + cc];
+                        }
+                }
+            }
+            if (parts > 1) __syncthreads();
+        }
+        const bool whole = seg == r.tiles;
+        if (warp == 0) {
+            const int gid = lane >> 2, t = lane & 3;
+            const int rb = item / heads, head = item - rb * heads;
+            const size_t slot = (2 * static_cast<size_t>(cta) + (t0 == 0 ? 1 : 0)) * C::kRows;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    const int col = 8 * n + 2 * t + cc;
+                    const int row = rb * C::kRows + col;
+                    if (row >= r.nq * p.group) continue;
+                    if (whole) {
+                        const float inv = w.l[n][cc] > 0.0f ? 1.0f / w.l[n][cc] : 0.0f;
+                        const int i = row / p.group;
+                        __half *dst = a.out + (static_cast<int64_t>(r.q0 + i) * a.q_heads + head * p.group + row - i * p.group) * D +
+                                      gid * (D / 8);
+#pragma unroll
+                        for (int v = 0; v < D / 64; ++v) {
+                            const float *lo = &w.o[n][4 * v][0];
+                            uint4 x;
+                            x.x = pack2(lo[cc] * inv, lo[4 + cc] * inv);
+                            x.y = pack2(lo[8 + cc] * inv, lo[12 + cc] * inv);
+                            x.z = pack2(lo[2 + cc] * inv, lo[6 + cc] * inv);
+                            x.w = pack2(lo[10 + cc] * inv, lo[14 + cc] * inv);
+                            reinterpret_cast<uint4 *>(dst)[v] = x;
+                        }
+                    } else {
+                        if (gid == 0) p.ml[slot + col] = make_float2(w.m[n][cc], w.l[n][cc]);
+                        float *dst = p.part + (slot + col) * D + gid * (D / 8);
+#pragma unroll
+                        for (int v = 0; v < D / 64; ++v) {
+                            const float *lo = &w.o[n][4 * v][0];
+                            reinterpret_cast<float4 *>(dst)[2 * v] = make_float4(lo[cc], lo[4 + cc], lo[8 + cc], lo[12 + cc]);
+                            reinterpret_cast<float4 *>(dst)[2 * v + 1] = make_float4(lo[2 + cc], lo[6 + cc], lo[10 + cc], lo[14 + cc]);
+                        }
+                    }
+                }
+            if (t0 == 0 && !whole) {
+                // the item goes on in the CTAs up to the one that holds its last tile
+                split_tail = true;
+                if (lane == 0) {
+                    const uint32_t last = u + r.tiles - 1;
+                    const uint32_t big = rest * (share + 1);
+                    const uint32_t cl = last < big ? last / (share + 1) : rest + (last - big) / share;
+                    p.desc[cta] = Desc{static_cast<int>(cl - c) + 1, b, item, 0};
+                }
+            }
+        }
+        u += seg;
+        t0 = 0;
+        if (u < u1 && ++item >= r.items && b + 1 < a.tab.B) {
+            item = 0;
+            do r = request_at<C::kRows>(p, ++b);
+            while (r.items == 0 && b + 1 < a.tab.B);
+        }
+    }
+    if (warp == 0 && lane == 0 && !split_tail) p.desc[cta].count = 0;
+    if (dead && lane == 0)  // the copies in flight land before the CTA exits
+        for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+            mbar_wait_for(&bar[i % C::kStages], (i / C::kStages) & 1, kDrainLimitNs);
+}
+
+// Joins the parts of the items that were cut: CTA (c, y) takes rows of the item
+// that CTA c of the first kernel began, one warp per row.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) join_kernel(const Params p)
+{
+    constexpr int ROWS = 8 * NT;
+    constexpr int E = D / 32;  // channels per lane
+    pdl_wait();
+    const int cta = static_cast<int>(blockIdx.x);
+    const Desc d = p.desc[cta];
+    if (d.count == 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Request r = request_at<ROWS>(p, d.b);
+    const int heads = p.a.cache.heads;
+    const int rb = d.item / heads, head = d.item - rb * heads;
+    const int col = static_cast<int>(blockIdx.y) * kWarps + warp;
+    const int row = rb * ROWS + col;
+    if (row >= r.nq * p.group) return;
+    // part 0 is in the first CTA's second slot, part i in CTA c + i's first
+    auto slot = [&](int i) { return (2 * static_cast<size_t>(cta + i) + (i == 0 ? 1 : 0)) * ROWS + col; };
+    float top = -INFINITY;
+    for (int i = lane; i < d.count; i += 32) top = fmaxf(top, p.ml[slot(i)].x);
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    float l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < d.count; ++i) {
+        const float2 ml = p.ml[slot(i)];
+        const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+        l += ml.y * f;
+        const float *src = p.part + slot(i) * D + E * lane;
+        if constexpr (E == 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(src);
+            o[0] += x.x * f; o[1] += x.y * f; o[2] += x.z * f; o[3] += x.w * f;
+        } else {
+            const float2 x = *reinterpret_cast<const float2 *>(src);
+            o[0] += x.x * f; o[1] += x.y * f;
+        }
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int i = row / p.group;
+    __half *dst = p.a.out + (static_cast<int64_t>(r.q0 + i) * p.a.q_heads + head * p.group + row - i * p.group) * D + E * lane;
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(dst) = pack2(o[0] * inv, o[1] * inv);
+}
+
+template <int D, int NT>
+cudaError_t configure_one()
+{
+    return cudaFuncSetAttribute(attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Cfg<D, NT>::kSmem));
+}
+
+template <int D, int NT>
+cudaError_t launch_one(const Params &prm, int num_sms, cudaStream_t st)
+{
+    using C = Cfg<D, NT>;
+    int grid = num_sms * C::kCtasPerSm;
+    if (grid > kMaxCtas) grid = kMaxCtas;
+    attend_kernel<D, NT><<<grid, kThreads, C::kSmem, st>>>(prm);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, C::kRows / kWarps, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, prm);
+}
+
+constexpr size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+constexpr int kMaxRows = 16;
+constexpr size_t kDescBytes = round256(sizeof(Desc) * kMaxCtas);
+constexpr size_t kMlBytes = round256(sizeof(float2) * 2 * kMaxCtas * kMaxRows);
+
+}  // namespace
+
+cudaError_t configure_kv4_attend()
+{
+    const cudaError_t r[] = {configure_one<128, 1>(), configure_one<128, 2>(), configure_one<64, 1>(), configure_one<64, 2>()};
+    for (cudaError_t x : r)
+        if (x != cudaSuccess) return x;
+    return cudaSuccess;
+}
+
+size_t kv4_attend_workspace(int D)
+{
+    return kDescBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * static_cast<size_t>(D);
+}
+
+cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, void *ws, int num_sms, cudaStream_t st)
+{
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    Params prm{};
+    prm.a = a;
+    prm.desc = reinterpret_cast<Desc *>(w);
+    prm.ml = reinterpret_cast<float2 *>(w + kDescBytes);
+    prm.part = reinterpret_cast<float *>(w + kDescBytes + kMlBytes);
+    prm.group = a.q_heads / a.cache.heads;
+    // 8 query rows per key/value head fill one MMA column tile, more take two
+    const bool narrow = static_cast<int64_t>(a.max_new) * prm.group <= 8;
+    if (a.cache.D == 128)
+        return narrow ? launch_one<128, 1>(prm, num_sms, st) : launch_one<128, 2>(prm, num_sms, st);
+    return narrow ? launch_one<64, 1>(prm, num_sms, st) : launch_one<64, 2>(prm, num_sms, st);
+}
+
+}  // namespace awq

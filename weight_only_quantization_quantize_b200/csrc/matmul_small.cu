@@ -28,6 +28,7 @@
 //    (st.async, completion counted on the owner's mbarrier) and the owner sums
 //    them in rank order (deterministic).
 #include "awq_kernels.cuh"
+#include "epilogue.cuh"
 
 namespace awq {
 
@@ -53,6 +54,7 @@ struct Params {
     int meta_smem;     // 1: those are staged in shared memory; 0 (longer k ranges): read from global memory
     int recv_bytes;    // partials pushed to this CTA: [src rank][8 * MT tokens][128 / splits]
     UnpackConsts uk;
+    Epilogue epi;      // read by the instantiations with an epilogue only
 };
 
 // x / s for 8 consecutive channels, rounded to binary16, stored in the
@@ -94,7 +96,7 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
     return p + ((1024u - (a & 1023u)) & 1023u);
 }
 
-template <int MT, int S>
+template <int MT, int S, bool EPI>
 __global__ void __launch_bounds__(160, 1)
     small_m_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmX,
                    const Params p)
@@ -305,6 +307,7 @@ __global__ void __launch_bounds__(160, 1)
     // the bytes pushed to it before it reduces, hence before it exits).
     cluster_arrive_relaxed();
     if (!mbar_wait(recv_bar, 0) && threadIdx.x == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+    if constexpr (EPI) pdl_wait();  // every thread may read the residual
     const int lchunks = cpo / 8;
     for (int e = threadIdx.x; e < p.M * lchunks; e += kAllThreads) {
         const int tok = e / lchunks;
@@ -320,6 +323,10 @@ __global__ void __launch_bounds__(160, 1)
             v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
             v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
         }
+        if constexpr (EPI) {
+            epi_store8(p.epi, v, p.Y, tok, n, p.N);
+            continue;
+        }
         uint4 o;
         o.x = __half_as_ushort(__float2half_rn(v[0])) | (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(v[1]))) << 16);
         o.y = __half_as_ushort(__float2half_rn(v[2])) | (static_cast<uint32_t>(__half_as_ushort(__float2half_rn(v[3]))) << 16);
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(160, 1)
     cluster_wait_acquire();
 }
 
-template <int MT, int S>
+template <int MT, int S, bool EPI>
 cudaError_t launch_one(const SmallMPlan &plan, const CUtensorMap &tmQ, const CUtensorMap &tmX,
                        const Params &prm, cudaStream_t st)
 {
@@ -348,14 +355,23 @@ cudaError_t launch_one(const SmallMPlan &plan, const CUtensorMap &tmQ, const CUt
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, small_m_kernel<MT, S>, tmQ, tmX, prm);
+    return cudaLaunchKernelEx(&cfg, small_m_kernel<MT, S, EPI>, tmQ, tmX, prm);
 }
 
 template <int MT, int S>
 cudaError_t configure_one()
 {
-    return cudaFuncSetAttribute(small_m_kernel<MT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                kSmemOptIn);
+    cudaError_t e = cudaFuncSetAttribute(small_m_kernel<MT, S, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmemOptIn);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(small_m_kernel<MT, S, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOptIn);
+}
+
+template <int MT, int S>
+cudaError_t launch_either(const SmallMPlan &plan, const CUtensorMap &tmQ, const CUtensorMap &tmX, const Params &prm,
+                          bool epi, cudaStream_t st)
+{
+    return epi ? launch_one<MT, S, true>(plan, tmQ, tmX, prm, st) : launch_one<MT, S, false>(plan, tmQ, tmX, prm, st);
 }
 
 // steps (256 B) and zero words (64 B) per group of the largest k range, when
@@ -449,9 +465,11 @@ cudaError_t launch_prescale(const __half *X, const __half *s, int M, int K, __ha
 cudaError_t launch_small_m(const SmallMPlan &plan, const CUtensorMap &tmQ, const CUtensorMap &tmX,
                            const __half *X, const __half *s, const __half *scales,
                            const int32_t *zeros, __half *Y, int M, int K, int N,
-                           int32_t *status, cudaStream_t st)
+                           int32_t *status, const Epilogue *epi, cudaStream_t st)
 {
     Params prm{};
+    if (epi) prm.epi = *epi;
+    const bool e = epi != nullptr;
     prm.X = X;
     prm.s = s;
     prm.scales = scales;
@@ -471,21 +489,21 @@ cudaError_t launch_small_m(const SmallMPlan &plan, const CUtensorMap &tmQ, const
     prm.uk = unpack_consts();
     if (plan.stages == 3) {
         switch (plan.mt) {
-        case 1: return launch_one<1, 3>(plan, tmQ, tmX, prm, st);
-        case 2: return launch_one<2, 3>(plan, tmQ, tmX, prm, st);
-        case 3: return launch_one<3, 3>(plan, tmQ, tmX, prm, st);
+        case 1: return launch_either<1, 3>(plan, tmQ, tmX, prm, e, st);
+        case 2: return launch_either<2, 3>(plan, tmQ, tmX, prm, e, st);
+        case 3: return launch_either<3, 3>(plan, tmQ, tmX, prm, e, st);
         default: return cudaErrorInvalidValue;
         }
     }
     switch (plan.mt) {
-    case 1: return launch_one<1, 4>(plan, tmQ, tmX, prm, st);
-    case 2: return launch_one<2, 4>(plan, tmQ, tmX, prm, st);
-    case 3: return launch_one<3, 4>(plan, tmQ, tmX, prm, st);
-    case 4: return launch_one<4, 4>(plan, tmQ, tmX, prm, st);
-    case 5: return launch_one<5, 4>(plan, tmQ, tmX, prm, st);
-    case 6: return launch_one<6, 4>(plan, tmQ, tmX, prm, st);
-    case 7: return launch_one<7, 4>(plan, tmQ, tmX, prm, st);
-    case 8: return launch_one<8, 4>(plan, tmQ, tmX, prm, st);
+    case 1: return launch_either<1, 4>(plan, tmQ, tmX, prm, e, st);
+    case 2: return launch_either<2, 4>(plan, tmQ, tmX, prm, e, st);
+    case 3: return launch_either<3, 4>(plan, tmQ, tmX, prm, e, st);
+    case 4: return launch_either<4, 4>(plan, tmQ, tmX, prm, e, st);
+    case 5: return launch_either<5, 4>(plan, tmQ, tmX, prm, e, st);
+    case 6: return launch_either<6, 4>(plan, tmQ, tmX, prm, e, st);
+    case 7: return launch_either<7, 4>(plan, tmQ, tmX, prm, e, st);
+    case 8: return launch_either<8, 4>(plan, tmQ, tmX, prm, e, st);
     default: return cudaErrorInvalidValue;
     }
 }

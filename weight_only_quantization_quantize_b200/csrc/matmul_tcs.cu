@@ -34,6 +34,7 @@
 // (0,4),(1,5),(2,6),(3,7) on both operands (X' is stored that way by the
 // pre-pass), which leaves the sum unchanged.
 #include "awq_kernels.cuh"
+#include "epilogue.cuh"
 
 namespace awq {
 
@@ -68,6 +69,7 @@ struct Params {
     int splits;       // cluster size along K
     int stage_bytes;  // X' tile + packed words + metadata
     UnpackConsts uk;
+    Epilogue epi;     // read by the instantiation with an epilogue only
 };
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
@@ -76,6 +78,7 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
     return p + ((1024u - (a & 1023u)) & 1023u);
 }
 
+template <bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     tcs_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmQ,
                const Params p)
@@ -288,6 +291,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the bytes pushed to it before it reduces, hence before it exits).
     cluster_arrive_relaxed();
     if (!mbar_wait(recv_bar, 0) && threadIdx.x == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+    if constexpr (EPI) {
+        // columns in pairs (2j, 2j + 1): a gate and its column sit in one thread
+        pdl_wait();  // every thread may read the residual
+        const int pairs = cpo / 2;
+        const Epilogue &epi = p.epi;
+        for (int e = threadIdx.x; e < p.M * pairs; e += kThreads) {
+            const int tok = e / pairs;
+            const int lc = 2 * (e - tok * pairs);
+            const int n = n0 + split * cpo + lc;
+            if (n >= p.N) continue;
+            float v0 = 0.0f, v1 = 0.0f;
+            for (int r = 0; r < p.splits; ++r) {
+                const float2 x = *reinterpret_cast<const float2 *>(recv + (r * p.nt + tok) * cpo + lc);
+                v0 += x.x;
+                v1 += x.y;
+            }
+            v0 += epi_bias(epi, n);
+            v1 += epi_bias(epi, n + 1);
+            if (epi.gated) {
+                const size_t at = static_cast<size_t>(tok) * (p.N / 2) + n / 2;
+                v0 = epi_act(v0, epi.act) * v1;
+                if (epi.residual) v0 += __half2float(epi.residual[at]);
+                p.Y[at] = __float2half_rn(v0);
+            } else {
+                const size_t at = static_cast<size_t>(tok) * p.N + n;
+                v0 = epi_act(v0, epi.act);
+                v1 = epi_act(v1, epi.act);
+                if (epi.residual) {
+                    const uint32_t r = *reinterpret_cast<const uint32_t *>(epi.residual + at);
+                    v0 += half_lo(r);
+                    v1 += half_hi(r);
+                }
+                *reinterpret_cast<uint32_t *>(p.Y + at) = pack_half2(v0, v1);
+            }
+        }
+    } else
     for (int e = threadIdx.x; e < p.M * cpo; e += kThreads) {
         const int tok = e / cpo;
         const int lc = e - tok * cpo;
@@ -333,15 +372,18 @@ TcsPlan plan_tcs(int M, int K, int N, int num_sms)
 
 cudaError_t configure_tcs()
 {
-    return cudaFuncSetAttribute(tcs_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(plan_tcs(64, 128, 128, 1).smem));
+    const int smem = static_cast<int>(plan_tcs(64, 128, 128, 1).smem);
+    cudaError_t e = cudaFuncSetAttribute(tcs_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(tcs_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 cudaError_t launch_tcs(const TcsPlan &plan, const CUtensorMap &tmX, const CUtensorMap &tmQ,
                        const __half *scales, const int32_t *zeros, __half *Y, int M, int K, int N,
-                       int32_t *status, cudaStream_t st)
+                       int32_t *status, const Epilogue *epi, cudaStream_t st)
 {
-    Params prm{scales, zeros, Y, status, M, K, N, plan.nt, plan.splits, plan.stage_bytes, unpack_consts()};
+    Params prm{scales, zeros, Y, status, M, K, N, plan.nt, plan.splits, plan.stage_bytes, unpack_consts(), Epilogue{}};
+    if (epi) prm.epi = *epi;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.splits, plan.n_tiles, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
@@ -356,7 +398,8 @@ cudaError_t launch_tcs(const TcsPlan &plan, const CUtensorMap &tmX, const CUtens
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, tcs_kernel, tmX, tmQ, prm);
+    return epi ? cudaLaunchKernelEx(&cfg, tcs_kernel<true>, tmX, tmQ, prm)
+               : cudaLaunchKernelEx(&cfg, tcs_kernel<false>, tmX, tmQ, prm);
 }
 
 }  // namespace awq

@@ -31,6 +31,7 @@
 // pre-pass, the unpack produces the weights that way), which leaves the sum
 // unchanged.
 #include "awq_kernels.cuh"
+#include "epilogue.cuh"
 
 namespace awq {
 
@@ -62,6 +63,7 @@ struct TctParams {
     int32_t *status;
     int M, K, N;
     UnpackConsts uk;
+    Epilogue epi;  // read by the instantiations with an epilogue only
 };
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
@@ -70,7 +72,7 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
     return p + ((1024u - (a & 1023u)) & 1023u);
 }
 
-template <int BT>
+template <int BT, bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     tct_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmQ,
                const TctParams p)
@@ -262,7 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mrem <= 0) break;
                 uint32_t v[32];
                 tmem_ld32(tmem_base + lane_addr + c0, v);
-                if (n_in) {
+                if constexpr (EPI) {
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
+                    epi_store_column32(p.epi, f, p.Y, m0 + c0, mrem, n, p.N);
+                } else if (n_in) {
                     __half *dst = p.Y + static_cast<size_t>(m0 + c0) * p.N + n;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -306,22 +313,32 @@ TctPlan plan_tct(int M, int K, int N, int num_sms)
 
 cudaError_t configure_tct()
 {
-    cudaError_t e = cudaFuncSetAttribute(tct_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(TctCfg<256>::kSmem));
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(tct_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(TctCfg<128>::kSmem));
+    const int s256 = static_cast<int>(TctCfg<256>::kSmem), s128 = static_cast<int>(TctCfg<128>::kSmem);
+    const cudaError_t r[] = {
+        cudaFuncSetAttribute(tct_kernel<256, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, s256),
+        cudaFuncSetAttribute(tct_kernel<256, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, s256),
+        cudaFuncSetAttribute(tct_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, s128),
+        cudaFuncSetAttribute(tct_kernel<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, s128)};
+    for (cudaError_t x : r)
+        if (x != cudaSuccess) return x;
+    return cudaSuccess;
 }
 
 cudaError_t launch_tct(const TctPlan &plan, const CUtensorMap &tmX, const CUtensorMap &tmQ, const __half *scales,
-                       const int32_t *zeros, __half *Y, int M, int K, int N, int32_t *status, cudaStream_t st)
+                       const int32_t *zeros, __half *Y, int M, int K, int N, int32_t *status,
+                       const Epilogue *epi, cudaStream_t st)
 {
-    TctParams prm{scales, zeros, Y, status, M, K, N, unpack_consts()};
+    TctParams prm{scales, zeros, Y, status, M, K, N, unpack_consts(), Epilogue{}};
+    if (epi) prm.epi = *epi;
     dim3 grid(plan.n_tiles, plan.m_tiles);
-    if (plan.bt == 256)
-        tct_kernel<256><<<grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+    if (plan.bt == 256 && epi)
+        tct_kernel<256, true><<<grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+    else if (plan.bt == 256)
+        tct_kernel<256, false><<<grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+    else if (epi)
+        tct_kernel<128, true><<<grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
     else
-        tct_kernel<128><<<grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+        tct_kernel<128, false><<<grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
     return cudaGetLastError();
 }
 

@@ -37,6 +37,7 @@
 // pre-pass, the unpack produces the weights that way), which leaves the sum
 // unchanged.
 #include "awq_kernels.cuh"
+#include "epilogue.cuh"
 
 namespace awq {
 
@@ -77,6 +78,7 @@ struct TskParams {
     int M, K, N;
     int n_tiles, m_tiles;
     UnpackConsts uk;
+    Epilogue epi;  // read by the instantiations with an epilogue only
 };
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p)
@@ -151,7 +153,7 @@ __device__ __forceinline__ void add_partials(float (&v)[32], const float *const 
         for (int i = 0; i < 32; ++i) v[i] += q[b][i];
 }
 
-template <int BT>
+template <int BT, bool EPI>
 __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
     tsk_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmQ,
                const TskParams p)
@@ -450,7 +452,9 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
                         const float *const sl[1] = {base + c * kSlot};
                         add_partials<1>(v, sl, c0, mrem);
                     }
-                    if (n < p.N) {
+                    if constexpr (EPI) {
+                        epi_store_column32(p.epi, v, p.Y, m0 + c0, mrem, n, p.N);
+                    } else if (n < p.N) {
                         __half *dst = p.Y + static_cast<size_t>(m0 + c0) * p.N + n;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -475,6 +479,16 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(C::kTmemCols)
                      : "memory");
     }
+}
+
+template <int BT, bool EPI>
+cudaError_t configure_tsk_one(int *ctas_per_sm)
+{
+    cudaError_t e = cudaFuncSetAttribute(tsk_kernel<BT, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(TskCfg<BT>::kSmem));
+    if (e != cudaSuccess) return e;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, tsk_kernel<BT, EPI>, kThreads,
+                                                         TskCfg<BT>::kSmem);
 }
 
 int tsk_bt(int M) { return M <= 128 ? 128 : 256; }
@@ -547,17 +561,15 @@ size_t tsk_partial_bytes(int M, int K, int N)
 
 cudaError_t configure_tsk()
 {
-    cudaError_t e = cudaFuncSetAttribute(tsk_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(TskCfg<256>::kSmem));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(tsk_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(TskCfg<128>::kSmem));
-    int n128 = 0, n256 = 0;
-    if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n128, tsk_kernel<128>, kThreads, TskCfg<128>::kSmem);
-    if (e == cudaSuccess)
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n256, tsk_kernel<256>, kThreads, TskCfg<256>::kSmem);
+    int n128 = 0, n256 = 0, e128 = 0, e256 = 0;
+    cudaError_t e = configure_tsk_one<256, false>(&n256);
+    if (e == cudaSuccess) e = configure_tsk_one<256, true>(&e256);
+    if (e == cudaSuccess) e = configure_tsk_one<128, false>(&n128);
+    if (e == cudaSuccess) e = configure_tsk_one<128, true>(&e128);
     if (e != cudaSuccess) return e;
+    // both kinds share the plan's grid
+    n128 = n128 < e128 ? n128 : e128;
+    n256 = n256 < e256 ? n256 : e256;
     if (n128 < 1 || n256 < 1) return cudaErrorInvalidConfiguration;
     // at most two 128-token CTAs (their TMEM takes 256 of the SM's 512 columns)
     g_ctas_per_sm[0] = n128 < 2 ? n128 : 2;
@@ -567,13 +579,19 @@ cudaError_t configure_tsk()
 
 cudaError_t launch_tsk(const TskPlan &plan, const CUtensorMap &tmX, const CUtensorMap &tmQ, const __half *scales,
                        const int32_t *zeros, __half *Y, int M, int K, int N, float *partials, uint32_t *flags,
-                       int32_t *status, cudaStream_t st)
+                       int32_t *status, const Epilogue *epi, cudaStream_t st)
 {
-    TskParams prm{scales, zeros, Y, status, partials, flags, M, K, N, plan.n_tiles, plan.m_tiles, unpack_consts()};
-    if (plan.bt == 256)
-        tsk_kernel<256><<<plan.grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+    TskParams prm{scales, zeros, Y, status, partials, flags, M, K, N, plan.n_tiles, plan.m_tiles, unpack_consts(),
+                  Epilogue{}};
+    if (epi) prm.epi = *epi;
+    if (plan.bt == 256 && epi)
+        tsk_kernel<256, true><<<plan.grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+    else if (plan.bt == 256)
+        tsk_kernel<256, false><<<plan.grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+    else if (epi)
+        tsk_kernel<128, true><<<plan.grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
     else
-        tsk_kernel<128><<<plan.grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
+        tsk_kernel<128, false><<<plan.grid, kThreads, plan.smem, st>>>(tmX, tmQ, prm);
     return cudaGetLastError();
 }
 
