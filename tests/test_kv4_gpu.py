@@ -1,0 +1,416 @@
+"""The paged 4-bit key/value cache on the GPU, against plain 64-bit statements.
+
+Page tables and stored bytes are exact; the attention is held to a bound that
+counts the kernel's roundings element by element (kv4_reference.attention).
+"""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_reference as ref
+import weight_only_quantization_quantize_b200 as awq
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows(T, H, D, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(T, H, D, generator=g)
+    x[..., ::29] *= 5
+    return x.half()
+
+
+def _bytes(t):
+    return t.cpu().numpy().copy()
+
+
+# ------------------------------------------------------------------ page tables
+@pytest.mark.parametrize("B,page,total_extra,cached,new", [
+    (1, 16, 0, 0, 1), (1, 64, 3, 0, 300), (3, 16, 5, 40, 9), (37, 32, 1, 500, 33), (513, 16, 7, 70, 1),
+    (4096, 16, 0, 33, 2), (100, 256, 11, 1000, 700), (9, 128, 0, 128, 128), (5, 16, 9000, 10, 4000)])
+def test_reserve_matches_a_plain_restatement(B, page, total_extra, cached, new):
+    r = random.Random(B * page + new)
+    lens = [r.randint(0, cached) for _ in range(B)]
+    add = [r.choice([0, new, r.randint(0, new)]) for _ in range(B)]
+    add[0] = new
+    held = [-(-n // page) for n in lens]
+    max_pages = -(-(cached + new) // page) + 1
+    num = sum(-(-(a + b) // page) for a, b in zip(lens, add)) + 3
+    order = list(range(num))
+    r.shuffle(order)
+    table = np.full((B, max_pages), -1, np.int32)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = order[at: at + h]
+        at += h
+    free = np.array(order[at:] + [-1] * at, np.int32)
+    total = sum(add) + total_extra
+    want = ref.reserve(add, lens, table, free, num - at, page, total)
+
+    def state():
+        return awq.KV4Pages(num, page, B, max_pages, block_table=torch.from_numpy(table).cuda(),
+                            lens=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                            free_pages=torch.from_numpy(free).cuda(),
+                            free_count=torch.tensor([num - at], dtype=torch.int32, device="cuda"))
+    nl = torch.tensor(add, dtype=torch.int32, device="cuda")
+    for in_place in (True, False):
+        p, st = state(), awq.new_status("cuda")
+        nxt = None if in_place else torch.full((B,), -5, dtype=torch.int32, device="cuda")
+        nf = None if in_place else torch.full((1,), -5, dtype=torch.int32, device="cuda")
+        slots, pos, cu = p.reserve(nl, total, next_lens=nxt, next_free=nf, status=st)
+        awq.raise_on_status(st)
+        got = (slots, pos, cu, p.lens if in_place else nxt, (p.free_count if in_place else nf), p.block_table)
+        for g, w, name in zip(got, want, ("slots", "positions", "cu", "lens", "free_count", "table")):
+            assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), name
+        if not in_place:
+            assert p.lens.tolist() == lens and int(p.free_count) == num - at
+            p.reserve(nl, total)   # the same step again, now in place
+            assert p.lens.tolist() == want[3].tolist()
+    # release some requests: pages go back in order
+    done = [int(r.random() < 0.5) for _ in range(B)]
+    st = awq.new_status("cuda")
+    p.release(torch.tensor(done, dtype=torch.int32, device="cuda"), status=st)
+    awq.raise_on_status(st)
+    back = [int(x) for b in range(B) if done[b] for x in want[5][b, : -(-int(want[3][b]) // page)]]
+    count = want[4] + len(back)
+    assert int(p.free_count) == count
+    assert p.free_pages.cpu().numpy()[:count].tolist() == free[: want[4]].tolist() + back
+    assert p.lens.tolist() == [0 if d else int(n) for d, n in zip(done, want[3])]
+    for b in range(B):
+        n = -(-int(want[3][b]) // page)
+        row = p.block_table[b].tolist()
+        assert row[:n] == ([-1] * n if done[b] else want[5][b, :n].tolist())
+
+
+def test_refused_steps_change_nothing():
+    def fresh():
+        return awq.KV4Pages(6, 16, 3, 4, lens=torch.tensor([17, 0, 5], dtype=torch.int32, device="cuda"),
+                            block_table=torch.tensor([[4, 1, -1, -1], [-1] * 4, [3, -1, -1, -1]], dtype=torch.int32, device="cuda"),
+                            free_pages=torch.tensor([0, 2, 5, -1, -1, -1], dtype=torch.int32, device="cuda"),
+                            free_count=torch.tensor([3], dtype=torch.int32, device="cuda"))
+    for add, total, code in [([16, 48, 0], 64, awq.ERR_CAPACITY), ([1, -1, 0], 10, awq.ERR_RANGE),
+                             ([48, 0, 0], 60, awq.ERR_RANGE), ([3, 3, 3], 8, awq.ERR_RANGE),
+                             ([2**31 - 1, 2**31 - 1, 2**31 - 1], 8, awq.ERR_RANGE)]:
+        p, st = fresh(), awq.new_status("cuda")
+        before = [t.clone() for t in (p.block_table, p.lens, p.free_pages, p.free_count)]
+        slots, pos, cu = p.reserve(torch.tensor(add, dtype=torch.int32, device="cuda"), total, status=st)
+        assert int(st) == code
+        assert bool((slots == -1).all()) and bool((pos == -1).all()) and bool((cu == 0).all())
+        for a, b in zip(before, (p.block_table, p.lens, p.free_pages, p.free_count)):
+            assert torch.equal(a, b)
+    p, st = fresh(), awq.new_status("cuda")
+    p.block_table[0, 1] = 99   # a page that the cache does not have
+    before = [t.clone() for t in (p.block_table, p.lens, p.free_pages, p.free_count)]
+    p.release(torch.ones(3, dtype=torch.int32, device="cuda"), status=st)
+    assert int(st) == awq.ERR_RANGE
+    for a, b in zip(before, (p.block_table, p.lens, p.free_pages, p.free_count)):
+        assert torch.equal(a, b)
+    p, st = fresh(), awq.new_status("cuda")
+    p.free_count.fill_(5)      # more pages than the cache has would be free
+    p.release(torch.ones(3, dtype=torch.int32, device="cuda"), status=st)
+    assert int(st) == awq.ERR_RANGE and int(p.free_count) == 5
+
+
+# ------------------------------------------------------------------ store and load
+def _edge_rows(x):
+    """Rows at the ends of the range: zeros, one sign, the largest, subnormals, one value."""
+    D = x.shape[-1]
+    edges = torch.stack([torch.zeros(D), torch.full((D,), 65504.0), torch.full((D,), -65504.0),
+                         torch.linspace(-65504, 65504, D), torch.linspace(5, 6, D), torch.linspace(-6, -5, D),
+                         torch.full((D,), 2.0**-24), torch.linspace(-2.0**-20, 2.0**-20, D), torch.full((D,), -0.0),
+                         torch.arange(D) % 16 / 4.0]).half()
+    n = min(len(edges), x.shape[0])
+    x[:n, 0] = edges[:n]
+    return x
+
+
+@pytest.mark.parametrize("T,H,D,page,fused", [(1, 1, 64, 16, False), (1, 8, 128, 16, True), (37, 3, 128, 32, True),
+                                              (130, 2, 64, 64, True), (515, 8, 128, 256, False), (64, 5, 64, 128, True)])
+def test_stored_bytes_and_values(T, H, D, page, fused):
+    k, v = _edge_rows(_rows(T, H, D, T)), _edge_rows(_rows(T, H, D, T + 1)).flip(0).contiguous()
+    pages = -(-T // page) + 2
+    p = awq.KV4Pages(pages, page, 1, pages)
+    c = awq.KV4Cache(p, H, D)
+    c.data.random_(0, 256)
+    want = _bytes(c.data)
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(T))[:T]
+    if T > 2:
+        slots[1] = -1
+        slots[T - 1] = -(1 << 40)
+    ref.store(want, k.numpy(), v.numpy(), slots.tolist(), page)
+    if fused:
+        row = torch.randn(T, 3 * H * D + 8).half().cuda()
+        row[:, H * D: 2 * H * D], row[:, 2 * H * D: 3 * H * D] = k.cuda().flatten(1), v.cuda().flatten(1)
+        kd, vd = row[:, H * D: 2 * H * D].unflatten(1, (H, D)), row[:, 2 * H * D: 3 * H * D]
+    else:
+        kd, vd = k.cuda(), v.cuda()
+    st = awq.new_status("cuda")
+    c.append(kd, vd, slots.cuda(), status=st)
+    awq.raise_on_status(st)
+    assert np.array_equal(_bytes(c.data), want)
+    # read back, a slot twice and one that holds nothing
+    ask = torch.cat([slots, slots[:1], torch.tensor([-3])])
+    gk, gv = c.load(ask.cuda(), status=st)
+    awq.raise_on_status(st)
+    real = (ask >= 0).numpy()
+    wk, wv, _, _ = ref.values(want, ask.clamp_min(0).numpy(), page, D)
+    for g, w in ((gk, wk), (gv, wv)):
+        w = torch.from_numpy(np.where(real[:, None, None], w, 0.0)).half()   # one rounding
+        assert torch.equal(g.cpu(), w)
+
+
+def test_bad_slots_and_values_are_reported():
+    H, D, page = 2, 64, 16
+    p = awq.KV4Pages(3, page, 1, 3)
+    c = awq.KV4Cache(p, H, D)
+    k, v = _rows(3, H, D, 1), _rows(3, H, D, 2)
+    want = _bytes(c.data)
+    slots = [5, 3 * page, 47]
+    ref.store(want, k.numpy()[[0, 2]], v.numpy()[[0, 2]], [5, 47], page)
+    st = awq.new_status("cuda")
+    c.append(k.cuda(), v.cuda(), torch.tensor(slots, device="cuda"), status=st)
+    assert int(st) == awq.ERR_RANGE
+    assert np.array_equal(_bytes(c.data), want)
+    st = awq.new_status("cuda")
+    gk, gv = c.load(torch.tensor([3 * page, 1 << 50], device="cuda"), status=st)
+    assert int(st) == awq.ERR_RANGE and not gk.any() and not gv.any()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for which in (0, 1):
+            x = [k.clone(), v.clone()]
+            x[which][1, 1, 7] = bad
+            st = awq.new_status("cuda")
+            c.append(x[0].cuda(), x[1].cuda(), torch.tensor([0, 1, 2], device="cuda"), status=st)
+            assert int(st) == awq.ERR_NONFINITE
+            # the other tokens are stored as ever
+            wk, wv, _, _ = ref.values(_bytes(c.data), [0, 2], page, D)
+            one = np.zeros_like(want)
+            ref.store(one, k.numpy(), v.numpy(), [0, 1, 2], page)
+            rk, rv, _, _ = ref.values(one, [0, 2], page, D)
+            assert np.array_equal(wk, rk) and np.array_equal(wv, rv)
+
+
+# ------------------------------------------------------------------ attention
+def _filled(lens, H, D, page, seed, spare=3, poison=True, max_pages=None):
+    """Pages and a cache with lens[b] tokens each; every unused byte poisoned (steps NaN, zero points 65535)."""
+    B = len(lens)
+    held = [-(-n // page) for n in lens]
+    num = sum(held) + spare
+    mp = max_pages or max(max(held), 1)
+    order = torch.randperm(num, generator=torch.Generator().manual_seed(seed)).to(torch.int32)
+    table = torch.full((B, mp), -1, dtype=torch.int32)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = order[at: at + h]
+        at += h
+    p = awq.KV4Pages(num, page, B, mp, block_table=table.cuda(), lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    data = torch.full((num, H, awq.kv4_page_bytes(page, D)), 0xFF if poison else 0, dtype=torch.uint8, device="cuda")
+    c = awq.KV4Cache(p, H, D, data=data)
+    slots = torch.cat([table[b].long()[torch.arange(n) // page] * page + torch.arange(n) % page
+                       for b, n in enumerate(lens)] or [torch.zeros(0, dtype=torch.long)])
+    if len(slots):
+        c.append(_rows(len(slots), H, D, seed + 1).cuda(), _rows(len(slots), H, D, seed + 2).cuda(), slots.cuda())
+    return p, c, table
+
+
+def _check_attention(c, table, q, cu, lens, max_new, window=0, scale=None, use_cu=True, extra_rows=0):
+    D = c.head_dim
+    T = q.shape[0]
+    scale = D ** -0.5 if scale is None else scale
+    out = torch.full((T, q.shape[1], D), 7.0, dtype=torch.float16, device="cuda")
+    st = awq.new_status("cuda")
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda") if use_cu else None
+    got = c.attention(q.cuda(), cu=cud, max_new=max_new, scale=scale, window=window, out=out, status=st)
+    awq.raise_on_status(st)
+    assert got is out
+    want, bound = ref.attention(q, _bytes(c.data), table.numpy(), lens, cu, c.pages.page_size, scale, window)
+    g = out.cpu().double()
+    n = cu[-1]
+    err = (g[:n] - want[:n]).abs()
+    assert bool((err <= bound[:n]).all()), float((err / bound[:n].clamp_min(1e-300)).max())
+    assert bool((g[n:] == 7.0).all()), "rows behind the last request"
+    return out
+
+
+@pytest.mark.parametrize("D,Hk,group,page", [(128, 2, 4, 16), (128, 1, 8, 64), (64, 3, 1, 32), (64, 2, 5, 16),
+                                             (128, 2, 7, 256), (128, 1, 16, 128), (64, 1, 40, 16), (128, 8, 1, 16)])
+@pytest.mark.parametrize("lens", [[1], [0, 1, 15, 16, 17, 31, 32, 33], [1000, 3, 0, 257], [4099]])
+def test_single_tokens(D, Hk, group, page, lens):
+    p, c, table = _filled(lens, Hk, D, page, seed=len(lens) + D + page)
+    q = _rows(len(lens) + 2, Hk * group, D, 9)
+    cu = list(range(len(lens) + 1))
+    a = _check_attention(c, table, q, cu, lens, 1)
+    b = _check_attention(c, table, q, cu, lens, 1, use_cu=False)
+    assert torch.equal(a, b)
+    _check_attention(c, table, q, cu, lens, 1, window=1)
+    _check_attention(c, table, q, cu, lens, 1, window=20, scale=0.3)
+
+
+@pytest.mark.parametrize("D,Hk,group,page", [(128, 2, 4, 16), (64, 2, 1, 32), (128, 1, 8, 64), (64, 1, 6, 16)])
+@pytest.mark.parametrize("lens,new", [([40, 5, 33], [3, 5, 1]), ([300, 64, 0, 17], [7, 0, 0, 17]), ([700], [90]),
+                                      ([130, 129, 1], [130, 65, 1]), ([515, 40], [33, 40])])
+def test_runs_of_tokens(D, Hk, group, page, lens, new):
+    p, c, table = _filled(lens, Hk, D, page, seed=sum(lens) + D)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = _rows(cu[-1] + 3, Hk * group, D, 11)
+    _check_attention(c, table, q, cu, lens, max(new))
+    _check_attention(c, table, q, cu, lens, max(new) + 500)
+    _check_attention(c, table, q, cu, lens, max(new), window=19)
+
+
+def test_more_queries_than_cached_tokens_and_empty_requests():
+    # queries before the first token see nothing and give zeros
+    p, c, table = _filled([3, 0], 2, 128, 16, seed=5)
+    q = _rows(9, 8, 128, 1)
+    out = _check_attention(c, table, q, [0, 5, 9], [3, 0], 5)
+    assert not out[:2].any() and not out[5:9].any()
+
+
+def test_large_and_small_magnitudes():
+    # keys and values at both ends of the format: no overflow of weights times steps, no loss to subnormals
+    H, D, page = 1, 128, 16
+    for kmag, vmag in [(1.0, 60000.0), (1.0, 2e-4), (1000.0, 1.0), (1e-3, 1e-3)]:
+        p, c, table = _filled([200], H, D, page, seed=3)
+        k, v = _rows(200, H, D, 1).float() / 25 * kmag, _rows(200, H, D, 2).float() / 25 * vmag
+        pos = torch.arange(200)
+        c.append(k.half().cuda(), v.half().cuda(), (table[0].long()[pos // page] * page + pos % page).cuda())
+        _check_attention(c, table, _rows(1, 8, D, 4), [0, 1], [200], 1)
+
+
+def test_strided_queries_and_out_of_order_streams():
+    lens, Hk, D = [77, 300], 2, 128
+    p, c, table = _filled(lens, Hk, D, 32, seed=8)
+    fused = _rows(2, 8 + 4, D, 3).cuda()
+    q = fused[:, :8]
+    want, bound = ref.attention(q, _bytes(c.data), table.numpy(), lens, [0, 1, 2], 32, D ** -0.5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = c.attention(q)
+    torch.cuda.current_stream().wait_stream(side)
+    assert bool(((out.cpu().double() - want).abs() <= bound).all())
+    assert torch.equal(out, c.attention(q))
+
+
+def test_bad_pages_and_lengths_are_reported_and_not_followed():
+    lens, Hk, D, page = [64, 40], 2, 64, 16
+    p, c, table = _filled(lens, Hk, D, page, seed=4)
+    q = _rows(2, 4, D, 2)
+    for bad in (-1, p.num_pages, 2**31 - 1):
+        p.block_table.copy_(table.cuda())
+        p.block_table[0, 3] = bad   # its tokens 48..63 are not seen
+        st = awq.new_status("cuda")
+        out = c.attention(q.cuda(), status=st)
+        assert int(st) == awq.ERR_RANGE
+        want, bound = ref.attention(q, _bytes(c.data), table.numpy(), [48, 40], [0, 1, 2], page, D ** -0.5)
+        assert bool(((out.cpu().double() - want).abs() <= bound).all())
+    p.block_table.copy_(table.cuda())
+    p.lens[1] = 1000   # longer than its row of the table: clamped, and the missing pages skipped
+    st = awq.new_status("cuda")
+    out = c.attention(q.cuda(), status=st)
+    assert int(st) == awq.ERR_RANGE
+    want, bound = ref.attention(q, _bytes(c.data), table.numpy(), [64, 40], [0, 1, 2], page, D ** -0.5)
+    assert bool(((out.cpu().double() - want)[0].abs() <= bound[0]).all())
+    p.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    for cu in ([0, 3, 2], [0, 1, 9], [-1, 1, 2]):
+        st = awq.new_status("cuda")
+        c.attention(q.cuda(), cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), max_new=2, status=st)
+        assert int(st) == awq.ERR_RANGE
+
+
+def test_offsets_beyond_32_bits():
+    # a cache of over 4 GB whose last pages are used, for store, load and attention
+    H, D, page = 8, 128, 16
+    num = (5 << 30) // (H * awq.kv4_page_bytes(page, D))
+    data = torch.empty(num, H, awq.kv4_page_bytes(page, D), dtype=torch.uint8, device="cuda")
+    table = torch.tensor([[num - 1, 2, num - 3, num // 2]], dtype=torch.int32)
+    p = awq.KV4Pages(num, page, 1, 4, block_table=table.cuda(), lens=torch.tensor([59], dtype=torch.int32, device="cuda"))
+    c = awq.KV4Cache(p, H, D, data=data)
+    pos = torch.arange(59)
+    slots = (table[0].long()[pos // page] * page + pos % page).cuda()
+    k, v = _rows(59, H, D, 1), _rows(59, H, D, 2)
+    c.append(k.cuda(), v.cuda(), slots)
+    gk, gv = c.load(slots)
+    small = np.zeros((4, H, awq.kv4_page_bytes(page, D)), np.uint8)
+    ref.store(small, k.numpy(), v.numpy(), pos.tolist(), page)
+    wk, wv, _, _ = ref.values(small, pos.numpy(), page, D)
+    assert torch.equal(gk.cpu(), torch.from_numpy(wk).half()) and torch.equal(gv.cpu(), torch.from_numpy(wv).half())
+    q = _rows(1, 16, D, 3)
+    want, bound = ref.attention(q, small, np.arange(4)[None], [59], [0, 1], page, D ** -0.5)
+    assert bool(((c.attention(q.cuda()).cpu().double() - want).abs() <= bound).all())
+
+
+def test_captured_graphs_follow_lengths_and_do_not_share_workspaces():
+    # two graphs captured on one stream, replayed at the same time on two others, with lengths changed in between
+    Hk, D, page = 4, 128, 16
+    made = []
+    side = torch.cuda.Stream()
+    for n in range(2):
+        p, c, table = _filled([900, 2000], Hk, D, page, seed=n)
+        q = _rows(2, 16, D, 5 + n).cuda()
+        out = torch.zeros(2, 16, D, dtype=torch.float16, device="cuda")
+        c.attention(q, out=out)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            c.attention(q, out=out)
+        made.append((g, p, c, table, q, out))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for lens in ([900, 2000], [513, 64], [1, 1999]):
+        for g, p, c, table, q, out in made:
+            p.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+            out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for (g, *_), s in zip(made, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for g, p, c, table, q, out in made:
+            want, bound = ref.attention(q.cpu(), _bytes(c.data), table.numpy(), lens, [0, 1, 2], page, D ** -0.5)
+            assert bool(((out.cpu().double() - want).abs() <= bound).all())
+            assert torch.equal(out, c.attention(q))   # the same bits as an eager call
+
+
+def test_arguments_are_checked_before_any_launch():
+    p, c, table = _filled([20], 2, 64, 16, seed=1)
+    q = _rows(1, 4, 64, 1).cuda()
+    out = torch.full((1, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    for bad in (dict(q=q[:, :3]), dict(q=q.float()), dict(q=q[..., :32]), dict(q=q.cpu()), dict(max_new=0), dict(window=-1),
+                dict(out=out[:, :2]), dict(out=out.float()), dict(cu=torch.zeros(3, dtype=torch.int32, device="cuda")),
+                dict(cu=torch.zeros(2, dtype=torch.int64, device="cuda")),
+                dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), dict(q=q[:0])):
+        args = dict(q=q, out=out)
+        args.update(bad)
+        with pytest.raises((TypeError, ValueError, awq.AwqError)):
+            c.attention(args.pop("q"), **args)
+    s = torch.zeros(1, dtype=torch.int64, device="cuda")
+    k = torch.zeros(1, 2, 64, dtype=torch.float16, device="cuda")
+    for bad in (dict(k=k.float()), dict(k=k[:, :1]), dict(v=k.cpu()), dict(slots=s.int()), dict(slots=s.new_zeros(2))):
+        args = dict(k=k, v=k, slots=s)
+        args.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            c.append(**args)
+    with pytest.raises(TypeError):
+        c.load(s.int())
+    with pytest.raises(ValueError):
+        c.load(s.view(1, 1))
+    nl = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad in (dict(total=0), dict(new_lens=nl.long()), dict(new_lens=nl.new_zeros(2)), dict(next_free=nl.new_zeros(2))):
+        args = dict(new_lens=nl, total=4)
+        args.update(bad)
+        with pytest.raises((TypeError, ValueError)):
+            p.reserve(**args)
+    with pytest.raises(ValueError):
+        awq.KV4Pages(4, 24, 1, 4)
+    with pytest.raises(ValueError):
+        awq.KV4Pages(4, 16, 4097, 4)
+    with pytest.raises(ValueError):
+        awq.KV4Pages(4, 16, 1, 2**27)
+    with pytest.raises(ValueError):
+        awq.KV4Cache(p, 2, 96)
+    with pytest.raises(ValueError):
+        awq.KV4Cache(p, 2, 64, data=torch.zeros(2, 2, 8, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert bool((out == 7.0).all())

@@ -3,20 +3,22 @@
 // HBM-bound regime, every cached code read once.
 //
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - max_j)
-//   k_j = step_j (c_j - z_j), and v_j likewise, so with the integer codes c
-//   q_i . k_j   = step_j (q_i . c_j - z_j sum(q_i))
-//   sum_j p v_j = sum_j (p_ij step_j) c_j - sum_j (p_ij step_j) z_j
-// Neither steps nor zero points enter the products: the tensor cores
-// (mma.sync m16n8k16, tokens or channels as rows, query rows as the 8 columns)
-// take the codes as they are packed.  A masked nibble 0x000F of a packed word
-// is the binary16 subnormal c 2^-24, and 0x00F0 is 16 c 2^-24, both exact, so
-// the unpack is one AND per pair of codes; the powers of two leave with the
-// accumulators.  A value needs the same channel of two tokens in one register:
-// one byte permute per pair of words gives that.
+//   k_j = step_j (c_j - z_j), and v_j likewise, with integer codes c, so
+//   q_i . k_j   = step_j (q_i . (c_j - z_j))
+//   sum_j p v_j = sum_j (p_ij step_j) (c_j - z_j)
+// The steps stay out of the products, whose operands c - z are exact in
+// binary16: the tensor cores (mma.sync m16n8k16, tokens or channels as rows,
+// query rows as the 8 columns) multiply integers, and the float accumulators
+// hold no offset that would have to cancel.  (Feeding the masked nibbles as
+// binary16 subnormals, without any unpacking arithmetic, was built first: the
+// tensor cores align subnormal products by their exponent field and lose 6 to
+// 10 bits of the sum.)  The unpack is one AND-OR per pair of codes into the
+// mantissa of 1024 and one packed add or multiply-add that takes 1024 (or 64)
+// and z off; integer and FMA pipes share it.  A value needs the same channel
+// of two tokens in one register: one byte permute per pair of words gives that.
 //
 // Roundings: p_ij step_j to binary16 for the second product (the row sum uses
-// the unrounded float p, the zero-point sum the rounded one, so that codes and
-// zero points cancel exactly), and the output.  The reference of the
+// the unrounded float p), and the output.  The reference of the
 // exponentials is kept on s + log2(step of v), and 2^8 above the largest
 // weight, so that the weights neither overflow (below 2^14 between two
 // updates) nor lose bits to subnormals within 2^-22 of the largest one.
@@ -68,6 +70,7 @@ struct Params {
     float2 *ml;      // [2 grid][rows]: (reference, sum) of a part
     float *part;     // [2 grid][rows][D]
     int group;
+    UnpackConsts uk;
 };
 
 struct Request {
@@ -151,11 +154,36 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ float2 unpack2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
-
 // (step, zero point) word of a token
 __device__ __forceinline__ float meta_step(uint32_t m) { return __half2float(__ushort_as_half(static_cast<uint16_t>(m))); }
-__device__ __forceinline__ float meta_zero(uint32_t m) { return __uint_as_float(0x4B000000u | (m >> 16)) - 8388608.0f; }
+// -(1024 + z) of two tokens' words (of one token: twice the same word), packed
+__device__ __forceinline__ uint32_t meta_zeros(uint32_t m0, uint32_t m1)
+{
+    return (__byte_perm(m0, m1, 0x7632) & 0x000F000Fu) | 0xE400E400u;  // finite, whatever the word holds
+}
+
+// Codes of a word's nibbles 0 and 4 (low) or 1 and 5 (high), as they lie in
+// both halves, minus zero points: za = -(1024 + z), zb = -(64 + z).
+__device__ __forceinline__ uint32_t codes_low(uint32_t w, uint32_t za, const UnpackConsts &k)
+{
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"((w & k.mask_lo) | k.magic), "r"(za));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t codes_high(uint32_t w, uint32_t zb, const UnpackConsts &k)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"((w & k.mask_hi) | k.magic), "r"(k.sixteenth), "r"(zb));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t zeros_high(uint32_t za)  // -(1024 + z) + 960
+{
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(za), "r"(0x63806380u));
+    return d;
+}
 // floor(log2(step)), and -14 for subnormal steps: step < 2^(this + 1)
 __device__ __forceinline__ float meta_exp(uint32_t m)
 {
@@ -172,9 +200,8 @@ __device__ __forceinline__ int token_of(int r) { return r ^ ((r >> 1) & 1); }
 template <int D, int NT>
 struct Warp {
     float o[NT][D / 16][4];     // numerators: [column tile][MMA][row/column]
-    float m[NT][2], l[NT][2], zs[NT][2];
+    float m[NT][2], l[NT][2];
     uint32_t q[NT][D / 32][2][2];  // the second operand of the first product
-    float sumq[NT][2];
     int hi[NT][2], lo[NT][2];   // keys lo < j <= hi of the lane's two rows
 };
 
@@ -196,7 +223,6 @@ __device__ __forceinline__ void start_item(Warp<D, NT> &w, const Params &p, cons
         const int i = in ? row / p.group : 0;
         const __half *src = p.a.q + (r.q0 + i) * p.a.q_stride +
                             static_cast<int64_t>(head * p.group + (in ? row - i * p.group : 0)) * D + 8 * (D / 32) * t;
-        float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
             const uint4 x = in ? __ldg(reinterpret_cast<const uint4 *>(src + 8 * k)) : make_uint4(0, 0, 0, 0);
@@ -205,16 +231,11 @@ __device__ __forceinline__ void start_item(Warp<D, NT> &w, const Params &p, cons
             w.q[n][k][0][1] = __byte_perm(x.y, x.w, 0x5410);
             w.q[n][k][1][0] = __byte_perm(x.x, x.z, 0x7632);
             w.q[n][k][1][1] = __byte_perm(x.y, x.w, 0x7632);
-            const float2 f0 = unpack2(x.x), f1 = unpack2(x.y), f2 = unpack2(x.z), f3 = unpack2(x.w);
-            sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            w.sumq[n][c] = __shfl_sync(0xffffffffu, sum, 4 * (2 * t + c));
             w.m[n][c] = -INFINITY;
-            w.l[n][c] = w.zs[n][c] = 0.0f;
+            w.l[n][c] = 0.0f;
             const int own = rb * ROWS + 8 * n + 2 * t + c;
             const int pos = max(r.len - r.nq + own / p.group, -1);  // -1: before the first token
             w.hi[n][c] = own < rows ? pos : -1;
@@ -227,7 +248,8 @@ __device__ __forceinline__ void start_item(Warp<D, NT> &w, const Params &p, cons
 // row; otherwise rows are masked and blocks whose bit in `have` is clear hold
 // nothing.
 template <int D, int NT>
-__device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int tok, bool full, int have, float c1, int lane)
+__device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int tok, bool full, int have, float c1,
+                                          const UnpackConsts &uk, int lane)
 {
     constexpr int KW = D / 32;  // key words per lane and row
     constexpr int VW = D / 64;  // value words per lane and token
@@ -245,6 +267,7 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
         const uint32_t ma = lds32(base + 16 * D + 4 * ra), mb = lds32(base + 16 * D + 4 * (ra + 8));
         vm[b][0] = lds32(base + 16 * D + 64 + 4 * ra);
         vm[b][1] = lds32(base + 16 * D + 64 + 4 * (ra + 8));
+        const uint32_t za = meta_zeros(ma, ma), zb = meta_zeros(mb, mb), ya = zeros_high(za), yb = zeros_high(zb);
         float al[NT][4], ah[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -253,8 +276,8 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
             const uint32_t a8 = ka[k] >> 8, b8 = kb[k] >> 8;
-            const uint32_t lo[4] = {ka[k] & 0x000F000Fu, kb[k] & 0x000F000Fu, a8 & 0x000F000Fu, b8 & 0x000F000Fu};
-            const uint32_t hi[4] = {ka[k] & 0x00F000F0u, kb[k] & 0x00F000F0u, a8 & 0x00F000F0u, b8 & 0x00F000F0u};
+            const uint32_t lo[4] = {codes_low(ka[k], za, uk), codes_low(kb[k], zb, uk), codes_low(a8, za, uk), codes_low(b8, zb, uk)};
+            const uint32_t hi[4] = {codes_high(ka[k], ya, uk), codes_high(kb[k], yb, uk), codes_high(a8, ya, uk), codes_high(b8, yb, uk)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 mma_16816(al[n], lo, w.q[n][k][0][0], w.q[n][k][0][1]);
@@ -262,13 +285,12 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
             }
         }
         const float fa = meta_step(ma) * c1, fb = meta_step(mb) * c1;
-        const float za = fa * meta_zero(ma) * 0x1p-24f, zb = fb * meta_zero(mb) * 0x1p-24f;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                s[b][n][c] = fmaf(fa, al[n][c], fmaf(fa * 0.0625f, ah[n][c], -za * w.sumq[n][c]));
-                s[b][n][2 + c] = fmaf(fb, al[n][2 + c], fmaf(fb * 0.0625f, ah[n][2 + c], -zb * w.sumq[n][c]));
+                s[b][n][c] = fa * (al[n][c] + ah[n][c]);
+                s[b][n][2 + c] = fb * (al[n][2 + c] + ah[n][2 + c]);
             }
     }
     if (!full) {
@@ -317,7 +339,6 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
                     const float f = ex2(w.m[n][c] - next);  // 0 for the first one
                     w.m[n][c] = next;
                     w.l[n][c] *= f;
-                    w.zs[n][c] *= f;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
                         w.o[n][i][c] *= f;
@@ -331,7 +352,7 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
     for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float step = meta_step(vm[b][h]), zero = meta_zero(vm[b][h]);
+            const float step = meta_step(vm[b][h]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float pv[2];
@@ -342,17 +363,17 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
                     w.l[n][c] += e;
                     pv[c] = full || x != -INFINITY ? e * step : 0.0f;
                 }
-                const uint32_t pk = pack2(pv[0], pv[1]);
-                const float2 pr = unpack2(pk);
-                w.zs[n][0] = fmaf(pr.x, zero, w.zs[n][0]);
-                w.zs[n][1] = fmaf(pr.y, zero, w.zs[n][1]);
-                pb[b][n][h] = transpose8x8(pk);
+                pb[b][n][h] = transpose8x8(pack2(pv[0], pv[1]));
             }
         }
     const int t0 = token_of(2 * t), t1 = token_of(2 * t + 1);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         const uint32_t base = stage + b * kv4_block_bytes(D) + 8 * D + gid * (4 * VW);
+        const uint32_t meta = stage + b * kv4_block_bytes(D) + 16 * D + 64;
+        const uint32_t z0 = meta_zeros(lds32(meta + 4 * t0), lds32(meta + 4 * t1));
+        const uint32_t z1 = meta_zeros(lds32(meta + 4 * (t0 + 8)), lds32(meta + 4 * (t1 + 8)));
+        const uint32_t y0 = zeros_high(z0), y1 = zeros_high(z1);
         uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
         lds_words<VW>(base + t0 * RB, v0);
         lds_words<VW>(base + t1 * RB, v1);
@@ -364,9 +385,12 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
                                    __byte_perm(v2[i], v3[i], 0x5410), __byte_perm(v2[i], v3[i], 0x7632)};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint32_t mask = (j & 1) ? 0x00F000F0u : 0x000F000Fu;
                 const int sh = (j & 2) ? 8 : 0;
-                const uint32_t a[4] = {(u[0] >> sh) & mask, (u[1] >> sh) & mask, (u[2] >> sh) & mask, (u[3] >> sh) & mask};
+                uint32_t a[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    a[e] = (j & 1) ? codes_high(u[e] >> sh, e < 2 ? y0 : y1, uk)
+                                     : codes_low(u[e] >> sh, e < 2 ? z0 : z1, uk);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) mma_16816(w.o[n][4 * i + j], a, pb[b][n][0], pb[b][n][1]);
             }
@@ -537,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
     int used = 0;
     bool dead = false;
     bool split_tail = false;
-    const float c1 = a.scale * kLog2e * 0x1p24f;
+    const float c1 = a.scale * kLog2e;
     Warp<D, NT> w;
     while (u < u1) {
         const int seg = static_cast<int>(min(static_cast<uint32_t>(r.tiles - t0), u1 - u));
@@ -558,9 +582,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
                 const int tok = (r.tile0 + t0 + k) * kTile;
                 const bool full = have == 3 && tok + kTile - 1 <= pfirst && tok > wlast;
                 if (full)
-                    tile_step<D, NT>(w, ring + st * C::kStage, tok, true, 3, c1, lane);
+                    tile_step<D, NT>(w, ring + st * C::kStage, tok, true, 3, c1, p.uk, lane);
                 else
-                    tile_step<D, NT>(w, ring + st * C::kStage, tok, false, have, c1, lane);
+                    tile_step<D, NT>(w, ring + st * C::kStage, tok, false, have, c1, p.uk, lane);
                 ++used;
                 __syncwarp();
                 if (!dead) issue();
@@ -572,15 +596,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
 #pragma unroll
                 for (int cc = 0; cc < 2; ++cc) {
 #pragma unroll
-                    for (int d = 4; d < 32; d *= 2) {
-                        w.l[n][cc] += __shfl_xor_sync(0xffffffffu, w.l[n][cc], d);
-                        w.zs[n][cc] += __shfl_xor_sync(0xffffffffu, w.zs[n][cc], d);
-                    }
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            w.o[n][i][2 * h + cc] = w.o[n][i][2 * h + cc] * ((i & 1) ? 0x1p20f : 0x1p24f) - w.zs[n][cc];
+                    for (int d = 4; d < 32; d *= 2) w.l[n][cc] += __shfl_xor_sync(0xffffffffu, w.l[n][cc], d);
                 }
         }
         // the warps' parts, last warp first, into the first warp
@@ -792,6 +808,7 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, void *ws, int num_sms, cud
     prm.ml = reinterpret_cast<float2 *>(w + kDescBytes);
     prm.part = reinterpret_cast<float *>(w + kDescBytes + kMlBytes);
     prm.group = a.q_heads / a.cache.heads;
+    prm.uk = unpack_consts();
     // 8 query rows per key/value head fill one MMA column tile, more take two
     const bool narrow = static_cast<int64_t>(a.max_new) * prm.group <= 8;
     if (a.cache.D == 128)
