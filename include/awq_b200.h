@@ -492,7 +492,7 @@ AWQ_API awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_he
  *   q_heads % kv_heads == 0, both <= AWQ_KV4_MAX_HEADS; 1 <= B <=
  *   AWQ_KV4_MAX_REQUESTS; 1 <= T, max_new < 2^31; max_pages * page_size < 2^31;
  *   B * kv_heads * ceil(max_new * q_heads / kv_heads / 8) * (max_pages * page_size /
- *   32 + 1) < 2^32
+ *   32 + 4) < 2^32
  * The result depends on the number of SMs (which fixes the order of sums),
  * never on timing: the same call gives the same bits.
  * Device errors: AWQ_ERR_RANGE (a length above max_pages * page_size or negative:

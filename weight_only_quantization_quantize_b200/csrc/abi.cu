@@ -713,7 +713,7 @@ awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, i
         return AWQ_ERR_SHAPE;
     // the run of tiles that the kernel splits is counted in 32 bits
     const int64_t blocks = (max_new * (q_heads / kv_heads) + 7) / 8;
-    const int64_t tiles = max_pages * page_size / 32 + 1;
+    const int64_t tiles = max_pages * page_size / 32 + 4;
     if (blocks > (int64_t(1) << 32) / (B * kv_heads) / tiles) return AWQ_ERR_SHAPE;
     if (!aligned16(q) || q_stride % 8 || !aligned16(cache) || !aligned4(block_table) || !aligned4(lens) ||
         (cu && !aligned4(cu)) || !aligned16(out) || (workspace && !aligned16(workspace)) ||

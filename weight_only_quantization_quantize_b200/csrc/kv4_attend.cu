@@ -24,13 +24,13 @@
 // updates) nor lose bits to subnormals within 2^-22 of the largest one.
 //
 // Work split: the (request, row block, head) items of all requests form one
-// line of 32-token tiles, and every CTA takes an equal run of it, whatever the
+// line of 64-token tiles, and every CTA takes an equal run of it, whatever the
 // lengths.  Runs that cut an item leave (max, sum, numerator) in the workspace
 // and a second kernel joins them in a fixed order: no atomics, no waiting
 // between CTAs, the same bits every time.
 //
 // A CTA is four independent warps with a ring of kStages tiles each, filled by
-// bulk copies that the warp's first lane issues: a block of 16 tokens (keys,
+// bulk copies that the warp's lanes issue in turn: a block of 16 tokens (keys,
 // values, steps, zero points) is one contiguous piece of the page.
 #include "awq_kernels.cuh"
 #include "kv4.cuh"
@@ -40,24 +40,30 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 32;       // tokens per ring stage: two blocks
+constexpr int kTile = 64;       // tokens per ring stage
+constexpr int kTileBlocks = kTile / kKvBlock;
+// An item's start and end (queries in, joins of warps, output) in tiles: the
+// runs are equal in this measure.  48 ragged requests of 819..16384 tokens, 8
+// heads: 132 us at 0, 126 at 2, 117 at 4, 113 at 6 to 12.
+constexpr int kItemCost = 8;
 constexpr int kMaxCtas = 640;
 constexpr int kMinTiles = 4;    // tiles per CTA at least, one per warp
 constexpr float kGain = 8.0f;   // log2 of the largest weight after an update
-constexpr float kSlack = 13.0f; // log2 of the weight that forces an update
+constexpr float kSlack = 13.0f; // log2 of the weight, without its step's fraction, that forces one
+constexpr float kLimit = 16384.0f;  // weights above 2^(kSlack + 1) ask for it
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int NT>
 struct Cfg {
     static constexpr int kRows = 8 * NT;
-    static constexpr int kStages = 3;
+    static constexpr int kStages = 2;
     static constexpr int kBlock = kv4_block_bytes(D);
-    static constexpr int kStage = 2 * kBlock;
+    static constexpr int kStage = kTileBlocks * kBlock;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kMerge = 4 * 32 * (NT * (D / 16) * 4 + 4 * NT);  // floats of one warp
     static constexpr int kBars = 8 * kWarps * kStages;
     static constexpr size_t kSmem = 128 + kRing + kMerge + kBars + 4 * kWarps * kStages + 64;
-    static constexpr int kCtasPerSm = NT == 1 ? 4 : 2;
+    static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
 };
 
 struct Desc {
@@ -77,6 +83,7 @@ struct Request {
     int len, nq, q0;   // cached tokens, queries, first query row
     int tile0, tiles;  // first tile that any query reads, tiles from there
     int items;         // row blocks times heads
+    int units;         // of one item: its tiles, and kItemCost for what it costs besides
 };
 
 template <int ROWS>
@@ -105,6 +112,7 @@ __device__ __forceinline__ Request request_at(const Params &p, int b)
     const int t = (r.len + kTile - 1) / kTile - r.tile0;
     r.tiles = t < 1 ? 1 : t;  // rows that see nothing are still written
     r.items = (r.nq * p.group + ROWS - 1) / ROWS * a.cache.heads;
+    r.units = r.tiles + kItemCost;
     return r;
 }
 
@@ -122,28 +130,36 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
+// Plain loads, so that the compiler may move them between the waits.
+__device__ __forceinline__ uint32_t word_at(const uint8_t *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 template <int W>
-__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[W])
+__device__ __forceinline__ void words_at(const uint8_t *p, uint32_t (&w)[W])
 {
-    if constexpr (W == 4)
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
-    else if constexpr (W == 2)
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
-    else
-        w[0] = lds32(a);
+    if constexpr (W == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if constexpr (W == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x; w[1] = x.y;
+    } else {
+        w[0] = word_at(p);
+    }
+}
+
+// D = A * B
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -157,9 +173,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 // (step, zero point) word of a token
 __device__ __forceinline__ float meta_step(uint32_t m) { return __half2float(__ushort_as_half(static_cast<uint16_t>(m))); }
 // -(1024 + z) of two tokens' words (of one token: twice the same word), packed
-__device__ __forceinline__ uint32_t meta_zeros(uint32_t m0, uint32_t m1)
+// in this order, or swapped with the other selector
+constexpr uint32_t kInOrder = 0x7632, kSwapped = 0x3276;
+__device__ __forceinline__ uint32_t meta_zeros(uint32_t m0, uint32_t m1, uint32_t order)
 {
-    return (__byte_perm(m0, m1, 0x7632) & 0x000F000Fu) | 0xE400E400u;  // finite, whatever the word holds
+    return (__byte_perm(m0, m1, order) & 0x000F000Fu) | 0xE400E400u;  // finite, whatever the word holds
 }
 
 // Codes of a word's nibbles 0 and 4 (low) or 1 and 5 (high), as they lie in
@@ -234,21 +252,21 @@ __device__ __forceinline__ void start_item(Warp<D, NT> &w, const Params &p, cons
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            w.m[n][c] = -INFINITY;
             w.l[n][c] = 0.0f;
             const int own = rb * ROWS + 8 * n + 2 * t + c;
             const int pos = max(r.len - r.nq + own / p.group, -1);  // -1: before the first token
             w.hi[n][c] = own < rows ? pos : -1;
+            w.m[n][c] = own < rows ? -INFINITY : 0.0f;  // rows that stand for nothing are never written
             w.lo[n][c] = p.a.window > 0 ? pos - p.a.window : -1;
         }
     }
 }
 
-// One tile of 32 tokens tok .. tok + 31.  full: every token is seen by every
-// row; otherwise rows are masked and blocks whose bit in `have` is clear hold
-// nothing.
+// Two blocks, 32 tokens tok .. tok + 31.  full: every token is seen by every
+// row, and every row has a reference; otherwise rows are masked and blocks
+// whose bit in `have` is clear hold nothing.
 template <int D, int NT>
-__device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int tok, bool full, int have, float c1,
+__device__ __forceinline__ void tile_step(Warp<D, NT> &w, const uint8_t *stage, int tok, bool full, int have, float c1,
                                           const UnpackConsts &uk, int lane)
 {
     constexpr int KW = D / 32;  // key words per lane and row
@@ -256,23 +274,19 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
     constexpr int RB = D / 2;   // bytes of a row
     const int gid = lane >> 2, t = lane & 3;
     const int ra = token_of(gid);
-    float s[2][NT][4];
+    float s[2][NT][4], f[2][2];  // products of q and codes; what a token's step and the scale make of them
     uint32_t vm[2][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        const uint32_t base = stage + b * kv4_block_bytes(D);
+        const uint8_t *base = stage + b * kv4_block_bytes(D);
         uint32_t ka[KW], kb[KW];
-        lds_words<KW>(base + ra * RB + t * (4 * KW), ka);
-        lds_words<KW>(base + (ra + 8) * RB + t * (4 * KW), kb);
-        const uint32_t ma = lds32(base + 16 * D + 4 * ra), mb = lds32(base + 16 * D + 4 * (ra + 8));
-        vm[b][0] = lds32(base + 16 * D + 64 + 4 * ra);
-        vm[b][1] = lds32(base + 16 * D + 64 + 4 * (ra + 8));
-        const uint32_t za = meta_zeros(ma, ma), zb = meta_zeros(mb, mb), ya = zeros_high(za), yb = zeros_high(zb);
+        words_at<KW>(base + ra * RB + t * (4 * KW), ka);
+        words_at<KW>(base + (ra + 8) * RB + t * (4 * KW), kb);
+        const uint32_t ma = word_at(base + 16 * D + 4 * ra), mb = word_at(base + 16 * D + 4 * (ra + 8));
+        vm[b][0] = word_at(base + 16 * D + 64 + 4 * ra);
+        vm[b][1] = word_at(base + 16 * D + 64 + 4 * (ra + 8));
+        const uint32_t za = meta_zeros(ma, ma, kInOrder), zb = meta_zeros(mb, mb, kInOrder), ya = zeros_high(za), yb = zeros_high(zb);
         float al[NT][4], ah[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) al[n][c] = ah[n][c] = 0.0f;
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
             const uint32_t a8 = ka[k] >> 8, b8 = kb[k] >> 8;
@@ -280,105 +294,134 @@ __device__ __forceinline__ void tile_step(Warp<D, NT> &w, uint32_t stage, int to
             const uint32_t hi[4] = {codes_high(ka[k], ya, uk), codes_high(kb[k], yb, uk), codes_high(a8, ya, uk), codes_high(b8, yb, uk)};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                mma_16816(al[n], lo, w.q[n][k][0][0], w.q[n][k][0][1]);
-                mma_16816(ah[n], hi, w.q[n][k][1][0], w.q[n][k][1][1]);
-            }
-        }
-        const float fa = meta_step(ma) * c1, fb = meta_step(mb) * c1;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                s[b][n][c] = fa * (al[n][c] + ah[n][c]);
-                s[b][n][2 + c] = fb * (al[n][2 + c] + ah[n][2 + c]);
-            }
-    }
-    if (!full) {
-        // select, never multiply: what a masked place holds may be anything
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int ja = tok + 16 * b + ra;
-            const bool there = (have >> b) & 1;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    if (!(there && ja <= w.hi[n][c] && ja > w.lo[n][c])) s[b][n][c] = -INFINITY;
-                    if (!(there && ja + 8 <= w.hi[n][c] && ja + 8 > w.lo[n][c])) s[b][n][2 + c] = -INFINITY;
+                if (k == 0) {
+                    mma_first(al[n], lo, w.q[n][k][0][0], w.q[n][k][0][1]);
+                    mma_first(ah[n], hi, w.q[n][k][1][0], w.q[n][k][1][1]);
+                } else {
+                    mma_16816(al[n], lo, w.q[n][k][0][0], w.q[n][k][0][1]);
+                    mma_16816(ah[n], hi, w.q[n][k][1][0], w.q[n][k][1][1]);
                 }
+            }
         }
+        f[b][0] = meta_step(ma) * c1;
+        f[b][1] = meta_step(mb) * c1;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[b][n][c] = al[n][c] + ah[n][c];
     }
-    float ev[2][2];
+    // Weights with the reference as it stands.  It is moved, one vote per tile,
+    // only when a weight passes 2^(kSlack + 1).
+    uint32_t pk[2][NT][2];
+    float sum[NT][2];
+    bool over = !full;
+    if (full) {
+        __half2 big = __float2half2_rn(0.0f);
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+        for (int n = 0; n < NT; ++n) sum[n][0] = sum[n][1] = 0.0f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) ev[b][h] = meta_exp(vm[b][h]);
-    // the largest weight of the lane's rows; the reference moves only when one
-    // would pass 2^kSlack (one vote per tile instead of three exchanges per row)
-    float top[NT][2];
-    bool over = false;
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+            for (int h = 0; h < 2; ++h) {
+                const float step = meta_step(vm[b][h]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            top[n][c] = fmaxf(fmaxf(s[0][n][c] + ev[0][0], s[0][n][2 + c] + ev[0][1]),
-                              fmaxf(s[1][n][c] + ev[1][0], s[1][n][2 + c] + ev[1][1]));
-            over |= top[n][c] > w.m[n][c] + kSlack;
-        }
+                for (int n = 0; n < NT; ++n) {
+                    const float e0 = ex2(fmaf(f[b][h], s[b][n][2 * h], -w.m[n][0]));
+                    const float e1 = ex2(fmaf(f[b][h], s[b][n][2 * h + 1], -w.m[n][1]));
+                    sum[n][0] += e0;
+                    sum[n][1] += e1;
+                    pk[b][n][h] = pack2(e0 * step, e1 * step);
+                    big = __hmax2(big, *reinterpret_cast<__half2 *>(&pk[b][n][h]));
+                }
+            }
+        over = !__hble2(big, __float2half2_rn(kLimit));
+    }
     if (__any_sync(0xffffffffu, over)) {
+        // floor(log2(step)) of each value joins the logits: weights include their steps
+        float ev[2][2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ev[b][h] = meta_exp(vm[b][h]);
+                const int j = tok + 16 * b + 8 * h + ra;
+                const bool there = (have >> b) & 1;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        // select, never multiply: what a masked place holds may be anything
+                        const bool seen = full || (there && j <= w.hi[n][c] && j > w.lo[n][c]);
+                        s[b][n][2 * h + c] = seen ? f[b][h] * s[b][n][2 * h + c] : -INFINITY;
+                    }
+            }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                float x = top[n][c];
+                float x = fmaxf(fmaxf(s[0][n][c] + ev[0][0], s[0][n][2 + c] + ev[0][1]),
+                                fmaxf(s[1][n][c] + ev[1][0], s[1][n][2 + c] + ev[1][1]));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 if (x > w.m[n][c] + kSlack) {
                     const float next = x - kGain;
-                    const float f = ex2(w.m[n][c] - next);  // 0 for the first one
+                    const float g = ex2(w.m[n][c] - next);  // 0 for the first one
                     w.m[n][c] = next;
-                    w.l[n][c] *= f;
+                    w.l[n][c] *= g;
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
-                        w.o[n][i][c] *= f;
-                        w.o[n][i][2 + c] *= f;
+                        w.o[n][i][c] *= g;
+                        w.o[n][i][2 + c] *= g;
                     }
+                }
+                sum[n][c] = 0.0f;
+            }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float step = meta_step(vm[b][h]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float pv[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float x = s[b][n][2 * h + c];
+                        const float e = x == -INFINITY ? 0.0f : ex2(x - w.m[n][c]);
+                        sum[n][c] += e;
+                        pv[c] = x == -INFINITY ? 0.0f : e * step;
+                    }
+                    pk[b][n][h] = pack2(pv[0], pv[1]);
                 }
             }
     }
     uint32_t pb[2][NT][2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int n = 0; n < NT; ++n) {
+        w.l[n][0] += sum[n][0];
+        w.l[n][1] += sum[n][1];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float step = meta_step(vm[b][h]);
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float pv[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float x = s[b][n][2 * h + c];
-                    const float e = ex2(x - (w.m[n][c] == -INFINITY ? 0.0f : w.m[n][c]));
-                    w.l[n][c] += e;
-                    pv[c] = full || x != -INFINITY ? e * step : 0.0f;
-                }
-                pb[b][n][h] = transpose8x8(pack2(pv[0], pv[1]));
-            }
-        }
+            for (int h = 0; h < 2; ++h) pb[b][n][h] = transpose8x8(pk[b][n][h]);
+    }
     const int t0 = token_of(2 * t), t1 = token_of(2 * t + 1);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        const uint32_t base = stage + b * kv4_block_bytes(D) + 8 * D + gid * (4 * VW);
-        const uint32_t meta = stage + b * kv4_block_bytes(D) + 16 * D + 64;
-        const uint32_t z0 = meta_zeros(lds32(meta + 4 * t0), lds32(meta + 4 * t1));
-        const uint32_t z1 = meta_zeros(lds32(meta + 4 * (t0 + 8)), lds32(meta + 4 * (t1 + 8)));
+        const uint8_t *base = stage + b * kv4_block_bytes(D) + 8 * D + gid * (4 * VW);
+        const uint8_t *meta = stage + b * kv4_block_bytes(D) + 16 * D + 64;
+        uint32_t m0[2], m1[2];  // rows 2 t and 2 t + 1, t0 and t1 in some order, and those 8 on
+        words_at<2>(meta + 8 * t, m0);
+        words_at<2>(meta + 8 * t + 32, m1);
+        const uint32_t order = (t & 1) ? kSwapped : kInOrder;
+        const uint32_t z0 = meta_zeros(m0[0], m0[1], order), z1 = meta_zeros(m1[0], m1[1], order);
         const uint32_t y0 = zeros_high(z0), y1 = zeros_high(z1);
         uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
-        lds_words<VW>(base + t0 * RB, v0);
-        lds_words<VW>(base + t1 * RB, v1);
-        lds_words<VW>(base + (t0 + 8) * RB, v2);
-        lds_words<VW>(base + (t1 + 8) * RB, v3);
+        words_at<VW>(base + t0 * RB, v0);
+        words_at<VW>(base + t1 * RB, v1);
+        words_at<VW>(base + (t0 + 8) * RB, v2);
+        words_at<VW>(base + (t1 + 8) * RB, v3);
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
             const uint32_t u[4] = {__byte_perm(v0[i], v1[i], 0x5410), __byte_perm(v0[i], v1[i], 0x7632),
@@ -434,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
     uint32_t mine = 0;
     for (int j = 0; j < per && bfirst + j < a.tab.B; ++j) {
         const Request r = request_at<C::kRows>(p, bfirst + j);
-        mine += static_cast<uint32_t>(r.items) * r.tiles;
+        mine += static_cast<uint32_t>(r.items) * r.units;
     }
     uint32_t pre = mine;
 #pragma unroll
@@ -466,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
         int b = bfirst;
         for (; b + 1 < a.tab.B; ++b) {
             const Request r = request_at<C::kRows>(p, b);
-            const uint32_t n = static_cast<uint32_t>(r.items) * r.tiles;
+            const uint32_t n = static_cast<uint32_t>(r.items) * r.units;
             if (rem < n) break;
             rem -= n;
         }
@@ -478,22 +521,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
     // ---------------------------------------------------------------- the warp's loads
     const uint32_t ring = smem_u32(smem) + warp * (C::kStages * C::kStage);
     uint64_t *bar = bars + warp * C::kStages;
+    const uint32_t bar0 = smem_u32(bar);
     int *have_of = haves + warp * C::kStages;
     // load cursor: request, item, first tile of the segment (within the item),
     // the segment's tiles, the next one for this warp
     int lb = s_b;
     Request lr = request_at<C::kRows>(p, lb);
-    int litem = static_cast<int>(static_cast<uint32_t>(s_rem) / lr.tiles);
-    int lt0 = s_rem - litem * lr.tiles;
+    int litem = static_cast<int>(static_cast<uint32_t>(s_rem) / lr.units);
+    // the segment [v, v + n) of an item's units: tiles from max(v - kItemCost, 0)
+    int lv = s_rem - litem * lr.units;
+    uint32_t ln = min(static_cast<uint32_t>(lr.units - lv), u1 - u0);
+    int lt0 = max(lv - kItemCost, 0);
     uint32_t lu = u0;
-    int lseg = static_cast<int>(min(static_cast<uint32_t>(lr.tiles - lt0), u1 - u0));
+    int lseg = max(lv + static_cast<int>(ln) - kItemCost, 0) - lt0;
     int lnext = warp;
-    int pg0 = 0, pg1 = 0, pbatch = -1;  // pages of 32 of the warp's tiles, one per lane
-    int issued = 0;
+    // the blocks of 8 of the warp's tiles, one block per lane: lane 4 i + j copies
+    // `bytes` bytes of tile i (its blocks from j on, up to the next copy)
+    const uint8_t *src = nullptr;
+    uint32_t bytes = 0, expect = 0;
+    int held = 0;         // bits of the tile's blocks that are there
+    int turn = 8;         // the tile of the batch that is next
+    int issued = 0;       // tiles asked for; the ring slot of the next one
+    int ist = 0;
 
     auto issue = [&]() {
         while (lnext >= lseg) {  // on to the next segment
-            lu += lseg;
+            lu += ln;
+            ln = 0;
             if (lu >= u1) {
                 lseg = lnext = 0;
                 return;
@@ -504,49 +558,42 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
                 do lr = request_at<C::kRows>(p, ++lb);
                 while (lr.items == 0 && lb + 1 < a.tab.B);
             }
-            lseg = static_cast<int>(min(static_cast<uint32_t>(lr.tiles), u1 - lu));
+            ln = min(static_cast<uint32_t>(lr.units), u1 - lu);
+            lseg = max(static_cast<int>(ln) - kItemCost, 0);
             lnext = warp;
-            pbatch = -1;
+            turn = 8;
         }
-        const int k = lnext / kWarps;  // the warp's k-th tile of the segment
-        if ((k >> 5) != pbatch) {
-            pbatch = k >> 5;
-            const int tl = warp + kWarps * (32 * pbatch + lane);
-            const int tok = (lr.tile0 + lt0 + tl) * kTile;
-            const int32_t *row = a.tab.block_table + static_cast<size_t>(lb) * a.tab.max_pages;
-            pg0 = pg1 = -1;
-            if (tl < lseg && tok < lr.len) {
-                pg0 = row[tok >> a.cache.page_shift];
-                bool bad = pg0 < 0 || pg0 >= a.cache.num_pages;
-                if (tok + kKvBlock < lr.len) {
-                    pg1 = a.cache.page_shift > 4 ? pg0 : row[(tok >> 4) + 1];
-                    bad |= pg1 < 0 || pg1 >= a.cache.num_pages;
-                    if (pg1 >= a.cache.num_pages) pg1 = -1;
-                }
-                if (pg0 >= a.cache.num_pages) pg0 = -1;
-                if (bad) report(a.status, AWQ_ERR_RANGE);
-            }
-        }
-        const int g0 = __shfl_sync(0xffffffffu, pg0, k & 31), g1 = __shfl_sync(0xffffffffu, pg1, k & 31);
-        if (lane == 0) {
-            const int tok = (lr.tile0 + lt0 + lnext) * kTile;
-            const int head = litem % heads;
-            const int st = issued % C::kStages;
-            const uint32_t dst = ring + st * C::kStage, mb = smem_u32(&bar[st]);
+        if (turn == 8) {
+            turn = 0;
+            const int tl = lnext + kWarps * (lane >> 2), j = lane & 3;
+            const int tok = (lr.tile0 + lt0 + tl) * kTile + kKvBlock * j;
             const int sh = a.cache.page_shift - 4;
-            const int64_t at = (tok >> 4) & ((1 << sh) - 1);
-            const int n0 = g0 >= 0, n1 = g1 >= 0;
-            mbar_arrive_expect_tx(&bar[st], static_cast<uint32_t>(n0 + n1) * C::kBlock);
-            const uint8_t *s0 = a.cache.data + (((static_cast<int64_t>(g0) * heads + head) << sh) + at) * C::kBlock;
-            if (n0) bulk_load(dst, s0, n1 && sh > 0 ? 2 * C::kBlock : C::kBlock, mb);
-            if (n1 && !(n0 && sh > 0)) {
-                const uint8_t *s1 =
-                    a.cache.data + (((static_cast<int64_t>(g1) * heads + head) << sh) + (sh > 0 ? at + 1 : 0)) * C::kBlock;
-                bulk_load(dst + C::kBlock, s1, C::kBlock, mb);
+            bool there = false;
+            if (tl < lseg && tok < lr.len) {
+                const int page = a.tab.block_table[static_cast<size_t>(lb) * a.tab.max_pages + (tok >> a.cache.page_shift)];
+                there = page >= 0 && page < a.cache.num_pages;
+                if (!there) report(a.status, AWQ_ERR_RANGE);
+                const int64_t at = (tok >> 4) & ((1 << sh) - 1);
+                src = a.cache.data + (((static_cast<int64_t>(page) * heads + litem % heads) << sh) + at) * C::kBlock;
             }
-            have_of[st] = n0 | (n1 << 1);
+            held = (__ballot_sync(0xffffffffu, there) >> (lane & 28)) & 15;
+            expect = __popc(held) * C::kBlock;
+            // blocks of one page lie together: its first block's lane copies them all
+            const int run = sh > 2 ? 4 : 1 << sh;
+            bytes = there && j % run == 0 ? __popc((held >> j) & ((1 << run) - 1)) * C::kBlock : 0;
         }
+        if ((lane >> 2) == turn) {
+            const uint32_t mb = bar0 + 8 * ist;
+            if ((lane & 3) == 0) {
+                mbar_arrive_expect_tx(&bar[ist], expect);
+                have_of[ist] = held;
+            }
+            __syncwarp(15u << (4 * turn));  // the barrier expects the bytes before they can arrive
+            if (bytes) bulk_load(ring + ist * C::kStage + (lane & 3) * C::kBlock, src, bytes, mb);
+        }
+        ++turn;
         ++issued;
+        if (++ist == C::kStages) ist = 0;
         lnext += kWarps;
     };
     for (int i = 0; i < C::kStages; ++i) issue();
@@ -555,16 +602,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
     // ---------------------------------------------------------------- segments
     int b = s_b;
     Request r = request_at<C::kRows>(p, b);
-    int item = static_cast<int>(static_cast<uint32_t>(s_rem) / r.tiles);
-    int t0 = s_rem - item * r.tiles;
+    int item = static_cast<int>(static_cast<uint32_t>(s_rem) / r.units);
+    int v = s_rem - item * r.units;
     uint32_t u = u0;
-    int used = 0;
+    int st = 0;         // ring slot of the next tile and the parity of its use
+    uint32_t ph = 0;
     bool dead = false;
     bool split_tail = false;
     const float c1 = a.scale * kLog2e;
     Warp<D, NT> w;
     while (u < u1) {
-        const int seg = static_cast<int>(min(static_cast<uint32_t>(r.tiles - t0), u1 - u));
+        const int n = static_cast<int>(min(static_cast<uint32_t>(r.units - v), u1 - u));
+        const int t0 = max(v - kItemCost, 0);
+        const int seg = max(v + n - kItemCost, 0) - t0;
         if (warp < seg) {
             start_item<D, NT>(w, p, r, item, lane);
             const int rb = item / heads;
@@ -572,20 +622,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
             const int ilast = min((rb * C::kRows + C::kRows - 1) / p.group, r.nq - 1);
             const int pfirst = r.len - r.nq + ifirst;                       // the earliest row's position
             const int wlast = a.window > 0 ? max(r.len - r.nq + ilast, -1) - a.window : -1;
+            // tiles first .. last - 1 of the segment hold only tokens that every row sees
+            const int base = r.tile0 + t0;
+            const int first = (wlast + kTile) / kTile - base;  // the first tile that begins above wlast
+            const int last = min(r.len, pfirst + 1) / kTile - base;
+            bool ready = false;  // every row has a reference
             for (int k = warp; k < seg; k += kWarps) {
-                const int st = used % C::kStages;
-                if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar[st], (used / C::kStages) & 1))) {
+                if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar[st], ph))) {
                     dead = true;
                     if (lane == 0) report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
                 }
+                const uint8_t *stage = smem + warp * (C::kStages * C::kStage) + st * C::kStage;
                 const int have = have_of[st];
-                const int tok = (r.tile0 + t0 + k) * kTile;
-                const bool full = have == 3 && tok + kTile - 1 <= pfirst && tok > wlast;
-                if (full)
-                    tile_step<D, NT>(w, ring + st * C::kStage, tok, true, 3, c1, p.uk, lane);
-                else
-                    tile_step<D, NT>(w, ring + st * C::kStage, tok, false, have, c1, p.uk, lane);
-                ++used;
+                if (ready && have == (1 << kTileBlocks) - 1 && k >= first && k < last) {
+#pragma unroll
+                    for (int b = 0; b < kTileBlocks; b += 2)
+                        tile_step<D, NT>(w, stage + b * C::kBlock, 0, true, 3, c1, p.uk, lane);
+                } else {
+                    for (int b = 0; b < kTileBlocks; b += 2)
+                        if ((have >> b) & 3)
+                            tile_step<D, NT>(w, stage + b * C::kBlock, (base + k) * kTile + b * kKvBlock, false,
+                                             (have >> b) & 3, c1, p.uk, lane);
+                    bool set = true;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) set = set && w.m[n][0] != -INFINITY && w.m[n][1] != -INFINITY;
+                    ready = __all_sync(0xffffffffu, set);
+                }
+                if (++st == C::kStages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
                 __syncwarp();
                 if (!dead) issue();
                 __syncwarp();
@@ -639,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
             if (parts > 1) __syncthreads();
         }
         const bool whole = seg == r.tiles;
-        if (warp == 0) {
+        if (warp == 0 && seg > 0) {
             const int gid = lane >> 2, t = lane & 3;
             const int rb = item / heads, head = item - rb * heads;
             const size_t slot = (2 * static_cast<size_t>(cta) + (t0 == 0 ? 1 : 0)) * C::kRows;
@@ -680,15 +746,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
                 // the item goes on in the CTAs up to the one that holds its last tile
                 split_tail = true;
                 if (lane == 0) {
-                    const uint32_t last = u + r.tiles - 1;
+                    const uint32_t last = u - v + r.units - 1;
                     const uint32_t big = rest * (share + 1);
                     const uint32_t cl = last < big ? last / (share + 1) : rest + (last - big) / share;
                     p.desc[cta] = Desc{static_cast<int>(cl - c) + 1, b, item, 0};
                 }
             }
         }
-        u += seg;
-        t0 = 0;
+        u += n;
+        v = 0;
         if (u < u1 && ++item >= r.items && b + 1 < a.tab.B) {
             item = 0;
             do r = request_at<C::kRows>(p, ++b);
