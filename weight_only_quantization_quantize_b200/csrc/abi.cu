@@ -5,7 +5,7 @@
 // accounting and the choice of tile path.  Every step of the computation runs
 // in the kernels of quantize.cu, fold.cu, gemv.cu, matmul_small.cu,
 // matmul_tcs.cu, matmul_tct.cu, matmul_tsk.cu, search.cu, clip.cu, kv4_pages.cu,
-// kv4_store.cu and kv4_attend.cu.
+// kv4_store.cu, kv4_attend.cu and kv4_prefill.cu.
 #include <mutex>
 
 #include "awq_kernels.cuh"
@@ -76,7 +76,7 @@ awq_status_t device_ready(int *sms)
                 awq::configure_gemv() != cudaSuccess || awq::configure_quantize() != cudaSuccess ||
                 awq::configure_tcs() != cudaSuccess || awq::configure_search() != cudaSuccess ||
                 awq::configure_clip() != cudaSuccess || awq::configure_kv4_pages() != cudaSuccess ||
-                awq::configure_kv4_attend() != cudaSuccess) {
+                awq::configure_kv4_attend() != cudaSuccess || awq::configure_kv4_prefill() != cudaSuccess) {
                 cudaGetLastError();
                 return AWQ_ERR_CUDA;
             }
@@ -607,6 +607,8 @@ awq::Kv4Cache kv4_cache(const uint8_t *data, int64_t kv_heads, int64_t D, int64_
                          page_shift_of(page_size)};
 }
 
+constexpr int64_t kPrefillRows = 64;
+
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 }  // namespace
 
@@ -735,6 +737,8 @@ awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, i
     a.window = static_cast<int>(window);
     a.scale = scale;
     a.status = dev_status;
+    if (max_new * (q_heads / kv_heads) > kPrefillRows)
+        return from_cuda(awq::launch_kv4_prefill(a, static_cast<cudaStream_t>(stream)));
     return from_cuda(awq::launch_kv4_attend(a, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -68,4 +68,8 @@ cudaError_t configure_kv4_attend();
 size_t kv4_attend_workspace(int D);
 cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, void *ws, int num_sms, cudaStream_t st);
 
+// kv4_prefill.cu -- many query rows per key/value head: tcgen05
+cudaError_t configure_kv4_prefill();
+cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, cudaStream_t st);
+
 }  // namespace awq

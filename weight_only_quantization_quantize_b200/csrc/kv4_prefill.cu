@@ -1,0 +1,548 @@
+// kv4_prefill.cu -- attention over the paged 4-bit key/value cache for many
+// query rows per key/value head (prompts and chunks of prompts): the
+// tensor-bound regime, on the 5th-generation tensor cores.
+//
+//   S = Q C_k^T, p = exp2(step_k scale log2(e) S - m), O = (p step_v) C_v / sum p
+// with the integer codes minus zero points C (exact in binary16): the steps
+// multiply the logits and the weights in float, one multiply-add and one
+// multiply per element, and never enter the tensor cores' operands.
+// Roundings: p step_v to binary16 (the second product's operand), the output.
+//
+// One CTA = 256 query rows (query tokens times the heads of a group, so that a
+// tile of codes is unpacked once for all of them) of one key/value head, as two
+// 128-row tiles that take turns: while the tensor cores work for one, the
+// softmax of the other runs.  Keys come in tiles of 128 tokens.
+//   warps 0..3, 4..7   softmax of query tile 0 and 1, one row per thread:
+//                      logits from tensor memory, weights back into the same
+//                      columns (the second product takes them from there)
+//   warps 8..11        unpack: one token per thread, 64 bytes of key and of value
+//                      codes straight from global memory (the next tile's are in
+//                      registers while this one is written), into two swizzled
+//                      shared-memory buffers each
+//   warp 12            issues the MMAs (128 x 128 x 16 and 128 x D x 16)
+// Tensor memory: logits 2 x 128 columns, outputs 2 x D columns.  Values stay in
+// token order [token][channel]: the second product reads them as an MN-major
+// operand, so nothing is transposed.
+//
+// The row maximum is not computed: the weights use a standing reference, and
+// only when one would pass 2^14 (or a row has none yet) does a warp read its
+// logits again, move the reference and rescale its output rows.
+#include "awq_kernels.cuh"
+#include "kv4.cuh"
+
+namespace awq {
+namespace {
+
+constexpr int kRowsTile = 128;           // query rows per MMA tile
+constexpr int kRowsCta = 2 * kRowsTile;
+constexpr int kKeys = 128;               // tokens per tile
+constexpr int kStages = 2;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kUnpackWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kUnpackWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr float kGain = 8.0f, kSlack = 13.0f, kLimit = 16384.0f;  // as in the split kernel
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPanel = kKeys * 128;      // bytes of 128 rows x 64 binary16, 128-byte swizzle
+
+template <int D>
+struct Cfg {
+    static constexpr int kPanels = D / 64;
+    static constexpr int kTile = kPanels * kPanel;                 // a Q, K or V tile
+    static constexpr int kOCol = 2 * kKeys;                        // output columns after the logits
+    static constexpr int kTmemCols = 512;
+    static constexpr int kStepBytes = kStages * 2 * kKeys * 4;     // step_k scale log2(e), step_v
+    static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * kTile + kStepBytes + 256;
+};
+
+struct Params {
+    Kv4AttendArgs a;
+    int group;
+    UnpackConsts uk;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// codes minus zero point of nibbles 0, 4 (low) or 1, 5 (high) of w
+__device__ __forceinline__ uint32_t codes_low(uint32_t w, uint32_t za, const UnpackConsts &k)
+{
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"((w & k.mask_lo) | k.magic), "r"(za));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t codes_high(uint32_t w, uint32_t zb, const UnpackConsts &k)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"((w & k.mask_hi) | k.magic), "r"(k.sixteenth), "r"(zb));
+    return d;
+}
+
+// MN-major operand: rows of 64 consecutive n (128 bytes, swizzled), one row per
+// k; 8 rows make an atom, atoms 1024 bytes apart along k and kPanel along n.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(kPanel >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Barriers, in shared memory.
+struct Bars {
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
+{
+    using C = Cfg<D>;
+    constexpr int W = D / 8;  // packed words of a row
+    extern __shared__ uint8_t smem_dyn[];
+    const uint32_t raw = smem_u32(smem_dyn);
+    uint8_t *smem = smem_dyn + ((1024u - (raw & 1023u)) & 1023u);
+    uint8_t *sq = smem, *sk = sq + 2 * C::kTile, *sv = sk + kStages * C::kTile;
+    float *steps = reinterpret_cast<float *>(sv + kStages * C::kTile);
+    __shared__ Bars bars;
+    __shared__ uint32_t s_valid[kStages][4];  // tokens of the tile that are there
+    __shared__ uint32_t s_tmem;
+
+    const Kv4AttendArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // ---------------------------------------------------------------- this CTA's rows and keys
+    // later row blocks see more keys: they come first
+    const int b = static_cast<int>(blockIdx.z), head = static_cast<int>(blockIdx.y);
+    const int rb = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+    const long long most = static_cast<long long>(a.tab.max_pages) << a.cache.page_shift;
+    int len = a.tab.lens[b];
+    const int q0 = a.tab.cu ? a.tab.cu[b] : b;
+    const long long q1 = a.tab.cu ? a.tab.cu[b + 1] : b + 1;
+    const long long nql = q1 - q0;
+    const bool bad_rows = q0 < 0 || nql < 0 || q1 > a.T || nql > a.max_new;
+    if (threadIdx.x == 0 && rb == 0 && head == 0 && (bad_rows || len < 0 || len > most)) report(a.status, AWQ_ERR_RANGE);
+    const int nq = bad_rows ? 0 : static_cast<int>(nql);
+    len = len < 0 ? 0 : len > most ? static_cast<int>(most) : len;
+    const long long rows = static_cast<long long>(nq) * p.group;
+    const long long row0 = static_cast<long long>(rb) * kRowsCta;
+    if (row0 >= rows) return;
+    const int ntiles_q = row0 + kRowsTile < rows ? 2 : 1;
+    const int rlast = static_cast<int>((row0 + kRowsCta < rows ? row0 + kRowsCta : rows) - 1);
+    const int pfirst = max(len - nq + static_cast<int>(row0 / p.group), -1);  // positions; -1: before the first token
+    const int plast = max(len - nq + rlast / p.group, -1);
+    const int lo_first = a.window > 0 ? max(pfirst - a.window + 1, 0) : 0;
+    const int tile0 = lo_first / kKeys;
+    const int tiles = plast < 0 ? 0 : plast / kKeys + 1 - tile0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars.k_full[i], kUnpackWarps);
+            mbar_init(&bars.k_empty[i], 1 + 4 * ntiles_q);  // MMA commit, and the softmax warps (steps read)
+            mbar_init(&bars.v_full[i], kUnpackWarps);
+            mbar_init(&bars.v_empty[i], 1);                 // MMA commit
+        }
+        mbar_init(&bars.q_full, 4 * ntiles_q);
+        mbar_init(&bars.drain, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars.s_full[t], 1);
+            mbar_init(&bars.p_full[t], 4);
+            mbar_init(&bars.o_full[t], 1);
+        }
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "r"(C::kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+
+    if (warp < kSoftmaxWarps) {
+        // ------------------------------------------------------------ softmax
+        const int t = warp >> 2;
+        if (t < ntiles_q) {
+            const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+            const uint32_t ts = tmem + lanes + t * kKeys;
+            const uint32_t to = tmem + lanes + C::kOCol + t * D;
+            const int r = 32 * (warp & 3) + lane;  // row of the tile
+            const long long row = row0 + t * kRowsTile + r;
+            const bool in = row < rows;
+            const int qi = in ? static_cast<int>(row / p.group) : 0;
+            const int qh = head * p.group + (in ? static_cast<int>(row - static_cast<long long>(qi) * p.group) : 0);
+            // the query row into its swizzled tile, channels of each 8 in the
+            // order (0,4),(1,5),(2,6),(3,7) that the unpack gives the keys
+            {
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (q0 + qi) * a.q_stride + static_cast<int64_t>(qh) * D);
+                uint8_t *dst = sq + t * C::kTile + r * 128;
+#pragma unroll
+                for (int c = 0; c < W; ++c) {
+                    const uint4 x = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                    const uint4 y = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * kPanel + (((c & 7) ^ (r & 7)) << 4)) = y;
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.q_full);
+            }
+            const int pos = in ? max(len - nq + qi, -1) : -1;
+            const int lo = a.window > 0 ? pos - a.window : -1;
+            // positions of the tile's first and last row: a key tile that every
+            // row sees needs no mask
+            const long long rt = row0 + t * kRowsTile;
+            const long long re = rt + kRowsTile - 1 < rows - 1 ? rt + kRowsTile - 1 : rows - 1;
+            const int p_lo = max(len - nq + static_cast<int>(rt / p.group), -1);
+            const int w_hi = a.window > 0 ? max(len - nq + static_cast<int>(re / p.group), -1) - a.window : -1;
+            float m = in ? -INFINITY : 0.0f, l = 0.0f;
+            bool ok = true, ready = false;
+            for (int j = 0; j < tiles; ++j) {
+                const int st = j % kStages;
+                const uint32_t ph = (j / kStages) & 1;
+                bool w = mbar_wait(&bars.k_full[st], ph);  // the steps
+                if (w) w = mbar_wait(&bars.s_full[t], j & 1);
+                if (!__all_sync(0xffffffffu, w)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float *ks = steps + st * 2 * kKeys, *vs = ks + kKeys;
+                const int tok = (tile0 + j) * kKeys;
+                const uint32_t v0 = s_valid[st][0], v1 = s_valid[st][1], v2 = s_valid[st][2], v3 = s_valid[st][3];
+                const bool plain = ready && (v0 & v1 & v2 & v3) == 0xffffffffu && tok + kKeys - 1 <= p_lo && tok > w_hi;
+                uint32_t pk[kKeys / 2];
+                float sum = 0.0f;
+                bool over = !plain;
+                if (plain) {
+                    __half2 big = __float2half2_rn(0.0f);
+#pragma unroll
+                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(ts + c0, s);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 kf = *reinterpret_cast<const float4 *>(ks + c0 + c);
+                            const float4 vf = *reinterpret_cast<const float4 *>(vs + c0 + c);
+                            const float e0 = ex2(fmaf(__uint_as_float(s[c]), kf.x, -m));
+                            const float e1 = ex2(fmaf(__uint_as_float(s[c + 1]), kf.y, -m));
+                            const float e2 = ex2(fmaf(__uint_as_float(s[c + 2]), kf.z, -m));
+                            const float e3 = ex2(fmaf(__uint_as_float(s[c + 3]), kf.w, -m));
+                            sum += (e0 + e1) + (e2 + e3);
+                            const uint32_t x = pack2(e0 * vf.x, e1 * vf.y), y = pack2(e2 * vf.z, e3 * vf.w);
+                            pk[(c0 + c) / 2] = x;
+                            pk[(c0 + c) / 2 + 1] = y;
+                            big = __hmax2(big, __hmax2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y)));
+                        }
+                    }
+                    over = !__hble2(big, __float2half2_rn(kLimit));
+                }
+                if (__any_sync(0xffffffffu, over)) {
+                    // with masks: the largest weight with its step, the reference,
+                    // the output rows, and the weights once more
+                    auto seen = [&](int c) -> bool {
+                        const uint32_t v = c < 64 ? (c < 32 ? v0 : v1) : (c < 96 ? v2 : v3);
+                        return ((v >> (c & 31)) & 1u) && tok + c <= pos && tok + c > lo;
+                    };
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(ts + c0, s);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float ev = static_cast<float>(static_cast<int>(__float_as_uint(vs[c0 + c]) >> 23) - 127);
+                            if (seen(c0 + c)) top = fmaxf(top, fmaf(__uint_as_float(s[c]), ks[c0 + c], ev));
+                        }
+                    }
+                    float f = 1.0f;
+                    if (top > m + kSlack) {
+                        const float next = top - kGain;
+                        f = ex2(m - next);  // 0 for the first one
+                        m = next;
+                        l *= f;
+                    }
+                    if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                        // the output holds the earlier tiles' sums (their MMAs came before this tile's logits)
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c0, o);
+                            uint32_t x[16];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(o[16 * h + c]) * f);
+                                tmem_st16(to + c0 + 16 * h, x);
+                            }
+                        }
+                    }
+                    sum = 0.0f;
+#pragma unroll
+                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(ts + c0, s);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float pv[2];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                // select, never multiply: a masked place gives 0
+                                const float e = seen(c0 + c + h) ? ex2(fmaf(__uint_as_float(s[c + h]), ks[c0 + c + h], -m)) : 0.0f;
+                                sum += e;
+                                pv[h] = seen(c0 + c + h) ? e * vs[c0 + c + h] : 0.0f;
+                            }
+                            pk[(c0 + c) / 2] = pack2(pv[0], pv[1]);
+                        }
+                    }
+                    ready = __all_sync(0xffffffffu, m != -INFINITY);
+                }
+                l += sum;
+#pragma unroll
+                for (int c = 0; c < kKeys / 2; c += 16) {
+                    uint32_t x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = pk[c + i];
+                    tmem_st16(ts + c, x);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars.p_full[t]);
+                    mbar_arrive(&bars.k_empty[st]);
+                }
+            }
+            // -------------------------------------------------------- output
+            if (tiles > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_full[t], 0));
+            if (!ok) {
+                if (lane == 0) report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+            } else {
+                tc_fence_after();
+                const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + (static_cast<int64_t>(q0 + qi) * a.q_heads + qh) * D);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    if (tiles > 0)
+                        tmem_ld32(to + c0, o);
+                    else
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = 0u;
+                    if (in) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) {
+                            // columns hold channels 0, 4, 1, 5, 2, 6, 3, 7 of each 8
+                            float x[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(o[c + i]) * inv;
+                            dst[(c0 + c) / 8] = make_uint4(pack2(x[0], x[2]), pack2(x[4], x[6]), pack2(x[1], x[3]), pack2(x[5], x[7]));
+                        }
+                    }
+                }
+            }
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------ unpack
+        const int uw = warp - kSoftmaxWarps;
+        const int tok_in = 32 * uw + lane;  // token of the tile
+        const int sh = a.cache.page_shift - 4;
+        const int32_t *table = a.tab.block_table + static_cast<size_t>(b) * a.tab.max_pages;
+        const float c1 = a.scale * kLog2e;
+        const UnpackConsts uk = p.uk;
+        const int end = min(len, plast + 1);  // keys from here on are seen by no row
+        // codes and steps of tile j's token; false where there is none
+        auto fetch = [&](int j, uint4 (&kx)[W / 4], uint4 (&vx)[W / 4], uint32_t &km, uint32_t &vm) -> bool {
+            const int tok = (tile0 + j) * kKeys + tok_in;
+            bool there = j < tiles && tok < end;
+            if (there) {
+                const int page = table[tok >> a.cache.page_shift];
+                if (page < 0 || page >= a.cache.num_pages) {
+                    report(a.status, AWQ_ERR_RANGE);
+                    there = false;
+                } else {
+                    const int64_t block = ((static_cast<int64_t>(page) * a.cache.heads + head) << sh) + ((tok >> 4) & ((1 << sh) - 1));
+                    const uint8_t *src = a.cache.data + block * kv4_block_bytes(D);
+                    const uint4 *kr = reinterpret_cast<const uint4 *>(src + (tok & 15) * (D / 2));
+                    const uint4 *vr = reinterpret_cast<const uint4 *>(src + 8 * D + (tok & 15) * (D / 2));
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i) {
+                        kx[i] = kr[i];
+                        vx[i] = vr[i];
+                    }
+                    km = *reinterpret_cast<const uint32_t *>(src + 16 * D + 4 * (tok & 15));
+                    vm = *reinterpret_cast<const uint32_t *>(src + 16 * D + 64 + 4 * (tok & 15));
+                }
+            }
+            if (!there) {
+                // zero codes at zero point 0: finite, and masked by s_valid
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
+                km = vm = 0;
+            }
+            return there;
+        };
+        auto unpack = [&](uint8_t *tile, const uint4 (&x)[W / 4], uint32_t meta) {
+            const uint32_t z = (meta >> 16) & 15u;
+            uint32_t za, zb;
+            zero_constants(z, za, zb);
+            uint8_t *dst = tile + tok_in * 128;
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = 4 * i + k;
+                    const uint32_t w8 = w[k] >> 8;
+                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * kPanel + (((c & 7) ^ (tok_in & 7)) << 4)) =
+                        make_uint4(codes_low(w[k], za, uk), codes_high(w[k], zb, uk), codes_low(w8, za, uk), codes_high(w8, zb, uk));
+                }
+            }
+        };
+        bool ok = true;
+        uint4 kx[W / 4], vx[W / 4];
+        uint32_t km = 0, vm = 0;
+        bool there = fetch(0, kx, vx, km, vm);
+        for (int j = 0; j < tiles; ++j) {
+            const int st = j % kStages;
+            const uint32_t ph = ((j / kStages) & 1) ^ 1u;
+            uint4 kn[W / 4], vn[W / 4];
+            uint32_t kmn, vmn;
+            const bool next = fetch(j + 1, kn, vn, kmn, vmn);
+            bool w = j < kStages || mbar_wait(&bars.k_empty[st], ph);
+            if (!__all_sync(0xffffffffu, w)) {
+                ok = false;
+                break;
+            }
+            float *ks = steps + st * 2 * kKeys;
+            ks[tok_in] = __half2float(__ushort_as_half(static_cast<uint16_t>(km))) * c1;
+            ks[kKeys + tok_in] = __half2float(__ushort_as_half(static_cast<uint16_t>(vm)));
+            const uint32_t valid = __ballot_sync(0xffffffffu, there);
+            if (lane == 0) s_valid[st][uw] = valid;
+            unpack(sk + st * C::kTile, kx, km);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.k_full[st]);
+            w = j < kStages || mbar_wait(&bars.v_empty[st], ph);
+            if (!__all_sync(0xffffffffu, w)) {
+                ok = false;
+                break;
+            }
+            unpack(sv + st * C::kTile, vx, vm);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.v_full[st]);
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                kx[i] = kn[i];
+                vx[i] = vn[i];
+            }
+            km = kmn;
+            vm = vmn;
+            there = next;
+        }
+        if (!ok && lane == 0) report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+    } else if (lane == 0 && tiles > 0) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t id_s = tc_idesc_f16(kRowsTile, kKeys);
+        constexpr uint32_t id_o = tc_idesc_f16(kRowsTile, D) | (1u << 16);  // B is MN-major
+        const uint32_t q_at = smem_u32(sq), k_at = smem_u32(sk), v_at = smem_u32(sv);
+        auto logits = [&](int t, int st) {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+                const uint32_t off = (s >> 2) * kPanel + 32 * (s & 3);
+                tc_mma(tmem + t * kKeys, sw128_desc(q_at + t * C::kTile + off), sw128_desc(k_at + st * C::kTile + off), id_s,
+                       s > 0 ? 1u : 0u);
+            }
+            tc_commit(&bars.s_full[t]);
+        };
+        bool ok = mbar_wait(&bars.q_full, 0) && mbar_wait(&bars.k_full[0], 0);
+        if (ok) {
+            tc_fence_after();
+            for (int t = 0; t < ntiles_q; ++t) logits(t, 0);
+            tc_commit(&bars.k_empty[0]);
+        }
+        for (int j = 0; j < tiles && ok; ++j) {
+            const int st = j % kStages, sn = (j + 1) % kStages;
+            ok = mbar_wait(&bars.v_full[st], (j / kStages) & 1);
+            for (int t = 0; t < ntiles_q && ok; ++t) {
+                ok = mbar_wait(&bars.p_full[t], j & 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int s = 0; s < kKeys / 16; ++s)
+                    tc_mma_ta(tmem + C::kOCol + t * D, tmem + t * kKeys + 8 * s, mn_desc(v_at + st * C::kTile + 2048 * s), id_o,
+                              j > 0 || s > 0 ? 1u : 0u);
+                if (t == ntiles_q - 1) tc_commit(&bars.v_empty[st]);
+                if (j + 1 == tiles) {
+                    tc_commit(&bars.o_full[t]);
+                    continue;
+                }
+                if (t == 0) ok = mbar_wait(&bars.k_full[sn], ((j + 1) / kStages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                logits(t, sn);
+            }
+            if (ok && j + 1 < tiles) tc_commit(&bars.k_empty[sn]);
+        }
+        if (!ok) {
+            // every MMA issued completes before tensor memory is freed
+            report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+            tc_commit(&bars.drain);
+            mbar_wait_for(&bars.drain, 0, kDrainLimitNs);
+        }
+    }
+    __syncwarp();
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
+    }
+}
+
+}  // namespace
+
+cudaError_t configure_kv4_prefill()
+{
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Cfg<128>::kSmem));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(prefill_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Cfg<64>::kSmem));
+}
+
+cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, cudaStream_t st)
+{
+    Params prm{};
+    prm.a = a;
+    prm.group = a.q_heads / a.cache.heads;
+    prm.uk = unpack_consts();
+    const int64_t new_rows = a.max_new < a.T ? a.max_new : a.T;
+    const dim3 grid(static_cast<unsigned>((new_rows * prm.group + kRowsCta - 1) / kRowsCta),
+                    static_cast<unsigned>(a.cache.heads), static_cast<unsigned>(a.tab.B));
+    if (a.cache.D == 128)
+        prefill_kernel<128><<<grid, kThreads, Cfg<128>::kSmem, st>>>(prm);
+    else
+        prefill_kernel<64><<<grid, kThreads, Cfg<64>::kSmem, st>>>(prm);
+    return cudaGetLastError();
+}
+
+}  // namespace awq
