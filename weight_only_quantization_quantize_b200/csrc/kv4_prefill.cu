@@ -24,9 +24,11 @@
 // token order [token][channel]: the second product reads them as an MN-major
 // operand, so nothing is transposed.
 //
-// The row maximum is not computed: the weights use a standing reference, and
-// only when one would pass 2^14 (or a row has none yet) does a warp read its
-// logits again, move the reference and rescale its output rows.
+// The row maximum is not computed: the weights use a standing reference.  The sum
+// of a tile's weights, times the largest value step of the tile, tells whether
+// one could have passed 2^14; only then (or while a row has no reference yet, or
+// under a mask) a warp looks for the maximum, moves the reference, rescales its
+// output rows and computes the weights again.
 #include "awq_kernels.cuh"
 #include "kv4.cuh"
 
@@ -40,8 +42,13 @@ constexpr int kStages = 2;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kUnpackWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kUnpackWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr float kGain = 8.0f, kSlack = 13.0f, kLimit = 16384.0f;  // as in the split kernel
+constexpr int kThreads = 512;            // the issuer's warpgroup has three idle warps
+// registers per thread of each warpgroup; the launch gives 128 to every thread
+constexpr int kSoftmaxRegs = 168, kUnpackRegs = 104, kIssueRegs = 72;
+static_assert(256 * kSoftmaxRegs + 128 * kUnpackRegs + 128 * kIssueRegs <= kThreads * 128, "register shares");
+constexpr float kGain = 6.0f;       // log2 of the largest weight, steps included, after an update
+constexpr float kSlack = 13.0f;     // log2 of the one that asks for the next
+constexpr float kLimit = 16384.0f;  // a tile's weights that add up to less hold none above
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPanel = kKeys * 128;      // bytes of 128 rows x 64 binary16, 128-byte swizzle
 
@@ -73,6 +80,62 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// two floats at a time
+__device__ __forceinline__ uint64_t two(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 both(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 32 columns of tensor memory on their way into r; r may be used after
+// tmem_arrived(r).
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
 // codes minus zero point of nibbles 0, 4 (low) or 1, 5 (high) of w
@@ -107,6 +170,17 @@ struct Bars {
     uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
 };
 
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
 {
@@ -119,6 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
     float *steps = reinterpret_cast<float *>(sv + kStages * C::kTile);
     __shared__ Bars bars;
     __shared__ uint32_t s_valid[kStages][4];  // tokens of the tile that are there
+    __shared__ __align__(16) float s_vmax[kStages][4];  // the largest step of their values, by unpack warp
     __shared__ uint32_t s_tmem;
 
     const Kv4AttendArgs &a = p.a;
@@ -177,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
 
     if (warp < kSoftmaxWarps) {
         // ------------------------------------------------------------ softmax
+        more_registers<kSoftmaxRegs>();
         const int t = warp >> 2;
         if (t < ntiles_q) {
             const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -225,52 +301,72 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 tc_fence_after();
                 const float *ks = steps + st * 2 * kKeys, *vs = ks + kKeys;
                 const int tok = (tile0 + j) * kKeys;
-                const uint32_t v0 = s_valid[st][0], v1 = s_valid[st][1], v2 = s_valid[st][2], v3 = s_valid[st][3];
-                const bool plain = ready && (v0 & v1 & v2 & v3) == 0xffffffffu && tok + kKeys - 1 <= p_lo && tok > w_hi;
-                uint32_t pk[kKeys / 2];
-                float sum = 0.0f;
+                const bool plain = ready && (s_valid[st][0] & s_valid[st][1] & s_valid[st][2] & s_valid[st][3]) == 0xffffffffu && tok + kKeys - 1 <= p_lo && tok > w_hi;
+                const float4 vm4 = *reinterpret_cast<const float4 *>(s_vmax[st]);
+                const float vmax = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
                 bool over = !plain;
                 if (plain) {
-                    __half2 big = __float2half2_rn(0.0f);
+                    // the next 32 logits are on their way while these are worked on
+                    uint32_t x[2][32], pk[kKeys / 2];
+                    uint64_t sum0 = 0, sum1 = 0;
+                    const uint64_t nm = two(-m, -m);
+                    tmem_ld32_start(ts, x[0]);
+                    tmem_arrived(x[0]);
 #pragma unroll
                     for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                        uint32_t s[32];
-                        tmem_ld32(ts + c0, s);
+                        uint32_t(&y)[32] = x[(c0 / 32) & 1];
+                        if (c0 + 32 < kKeys) tmem_ld32_start(ts + c0 + 32, x[(c0 / 32 + 1) & 1]);
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            const float4 kf = *reinterpret_cast<const float4 *>(ks + c0 + c);
-                            const float4 vf = *reinterpret_cast<const float4 *>(vs + c0 + c);
-                            const float e0 = ex2(fmaf(__uint_as_float(s[c]), kf.x, -m));
-                            const float e1 = ex2(fmaf(__uint_as_float(s[c + 1]), kf.y, -m));
-                            const float e2 = ex2(fmaf(__uint_as_float(s[c + 2]), kf.z, -m));
-                            const float e3 = ex2(fmaf(__uint_as_float(s[c + 3]), kf.w, -m));
-                            sum += (e0 + e1) + (e2 + e3);
-                            const uint32_t x = pack2(e0 * vf.x, e1 * vf.y), y = pack2(e2 * vf.z, e3 * vf.w);
-                            pk[(c0 + c) / 2] = x;
-                            pk[(c0 + c) / 2 + 1] = y;
-                            big = __hmax2(big, __hmax2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y)));
+                            const ulonglong2 kf = *reinterpret_cast<const ulonglong2 *>(ks + c0 + c);
+                            const ulonglong2 vf = *reinterpret_cast<const ulonglong2 *>(vs + c0 + c);
+                            const float2 y0 = both(fma2(two(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), kf.x, nm));
+                            const float2 y1 = both(fma2(two(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), kf.y, nm));
+                            const uint64_t e0 = two(ex2(y0.x), ex2(y0.y)), e1 = two(ex2(y1.x), ex2(y1.y));
+                            sum0 = add2(sum0, e0);
+                            sum1 = add2(sum1, e1);
+                            const float2 w0 = both(mul2(e0, vf.x)), w1 = both(mul2(e1, vf.y));
+                            pk[(c0 + c) / 2] = pack2(w0.x, w0.y);
+                            pk[(c0 + c) / 2 + 1] = pack2(w1.x, w1.y);
+                        }
+                        if (c0 + 32 < kKeys) tmem_arrived(x[(c0 / 32 + 1) & 1]);
+                    }
+                    const float2 s2 = both(add2(sum0, sum1));
+                    const float sum = s2.x + s2.y;
+                    over = !(sum * vmax <= kLimit);
+                    over = __any_sync(0xffffffffu, over);
+                    if (!over) {
+                        l += sum;
+#pragma unroll
+                        for (int c = 0; c < kKeys / 2; c += 16) {
+                            uint32_t z[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) z[i] = pk[c + i];
+                            tmem_st16(ts + c, z);
                         }
                     }
-                    over = !__hble2(big, __float2half2_rn(kLimit));
                 }
-                if (__any_sync(0xffffffffu, over)) {
-                    // with masks: the largest weight with its step, the reference,
-                    // the output rows, and the weights once more
-                    auto seen = [&](int c) -> bool {
-                        const uint32_t v = c < 64 ? (c < 32 ? v0 : v1) : (c < 96 ? v2 : v3);
-                        return ((v >> (c & 31)) & 1u) && tok + c <= pos && tok + c > lo;
+                if (over) {
+                    // with masks: the maximum, the reference, the output rows, the weights; 16 keys at a time
+                    // the keys c with lo < tok + c <= pos, of those that are there
+                    auto seen16 = [&](int c0) -> uint32_t {
+                        const int up = pos - tok - c0, dn = lo - tok - c0;
+                        uint32_t seen = up < 0 ? 0u : up >= 15 ? 0xffffu : (2u << up) - 1u;
+                        if (dn >= 0) seen &= dn >= 15 ? 0u : ~((2u << dn) - 1u);
+                        return seen & (s_valid[st][c0 / 32] >> (c0 & 16));
                     };
                     float top = -INFINITY;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                        uint32_t s[32];
-                        tmem_ld32(ts + c0, s);
+                    for (int c0 = 0; c0 < kKeys; c0 += 16) {
+                        uint32_t y[16];
+                        tmem_ld16(ts + c0, y);
+                        const uint32_t seen = seen16(c0);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float ev = static_cast<float>(static_cast<int>(__float_as_uint(vs[c0 + c]) >> 23) - 127);
-                            if (seen(c0 + c)) top = fmaxf(top, fmaf(__uint_as_float(s[c]), ks[c0 + c], ev));
-                        }
+                        for (int c = 0; c < 16; ++c)
+                            if ((seen >> c) & 1u) top = fmaxf(top, __uint_as_float(y[c]) * ks[c0 + c]);
                     }
+                    // an upper bound of the weights' logarithms, steps included
+                    top += static_cast<float>(static_cast<int>(__float_as_uint(vmax) >> 23) - 126);
                     float f = 1.0f;
                     if (top > m + kSlack) {
                         const float next = top - kGain;
@@ -279,48 +375,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                         l *= f;
                     }
                     if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-                        // the output holds the earlier tiles' sums (their MMAs came before this tile's logits)
+                        // the earlier tiles' sums: their MMAs came before this tile's logits
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + c0, o);
-                            uint32_t x[16];
+                        for (int c0 = 0; c0 < D; c0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(to + c0, o);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(o[16 * h + c]) * f);
-                                tmem_st16(to + c0 + 16 * h, x);
-                            }
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(to + c0, o);
                         }
                     }
-                    sum = 0.0f;
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                        uint32_t s[32];
-                        tmem_ld32(ts + c0, s);
+                        uint32_t z[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            float pv[2];
+                        for (int g = 0; g < 32; g += 16) {
+                            uint32_t y[16];
+                            tmem_ld16(ts + c0 + g, y);
+                            const uint32_t seen = seen16(c0 + g);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                // select, never multiply: a masked place gives 0
-                                const float e = seen(c0 + c + h) ? ex2(fmaf(__uint_as_float(s[c + h]), ks[c0 + c + h], -m)) : 0.0f;
-                                sum += e;
-                                pv[h] = seen(c0 + c + h) ? e * vs[c0 + c + h] : 0.0f;
+                            for (int c = 0; c < 16; c += 2) {
+                                float pv[2];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    // select, never multiply: a masked place gives 0
+                                    const bool in_sight = (seen >> (c + h)) & 1u;
+                                    const float e = in_sight ? ex2(fmaf(__uint_as_float(y[c + h]), ks[c0 + g + c + h], -m)) : 0.0f;
+                                    l += e;
+                                    pv[h] = in_sight ? e * vs[c0 + g + c + h] : 0.0f;
+                                }
+                                z[(g + c) / 2] = pack2(pv[0], pv[1]);
                             }
-                            pk[(c0 + c) / 2] = pack2(pv[0], pv[1]);
                         }
+                        tmem_st16(ts + c0 / 2, z);  // over logits that have been read
                     }
-                    ready = __all_sync(0xffffffffu, m != -INFINITY);
                 }
-                l += sum;
-#pragma unroll
-                for (int c = 0; c < kKeys / 2; c += 16) {
-                    uint32_t x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = pk[c + i];
-                    tmem_st16(ts + c, x);
-                }
+                if (!ready) ready = __all_sync(0xffffffffu, m != -INFINITY);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -360,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
         }
     } else if (warp < kMmaWarp) {
         // ------------------------------------------------------------ unpack
+        fewer_registers<kUnpackRegs>();
         const int uw = warp - kSoftmaxWarps;
         const int tok_in = 32 * uw + lane;  // token of the tile
         const int sh = a.cache.page_shift - 4;
@@ -434,7 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
             ks[tok_in] = __half2float(__ushort_as_half(static_cast<uint16_t>(km))) * c1;
             ks[kKeys + tok_in] = __half2float(__ushort_as_half(static_cast<uint16_t>(vm)));
             const uint32_t valid = __ballot_sync(0xffffffffu, there);
-            if (lane == 0) s_valid[st][uw] = valid;
+            const uint32_t vtop = __reduce_max_sync(0xffffffffu, vm & 0xffffu);  // steps are positive: ordered as integers
+            if (lane == 0) {
+                s_valid[st][uw] = valid;
+                s_vmax[st][uw] = __half2float(__ushort_as_half(static_cast<uint16_t>(vtop)));
+            }
             unpack(sk + st * C::kTile, kx, km);
             fence_proxy_async();
             __syncwarp();
@@ -458,54 +553,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
             there = next;
         }
         if (!ok && lane == 0) report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
-    } else if (lane == 0 && tiles > 0) {
+    } else {
         // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t id_s = tc_idesc_f16(kRowsTile, kKeys);
-        constexpr uint32_t id_o = tc_idesc_f16(kRowsTile, D) | (1u << 16);  // B is MN-major
-        const uint32_t q_at = smem_u32(sq), k_at = smem_u32(sk), v_at = smem_u32(sv);
-        auto logits = [&](int t, int st) {
+        fewer_registers<kIssueRegs>();
+        if (warp == kMmaWarp && lane == 0 && tiles > 0) {
+            constexpr uint32_t id_s = tc_idesc_f16(kRowsTile, kKeys);
+            constexpr uint32_t id_o = tc_idesc_f16(kRowsTile, D) | (1u << 16);  // B is MN-major
+            const uint32_t q_at = smem_u32(sq), k_at = smem_u32(sk), v_at = smem_u32(sv);
+            auto logits = [&](int t, int st) {
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s) {
-                const uint32_t off = (s >> 2) * kPanel + 32 * (s & 3);
-                tc_mma(tmem + t * kKeys, sw128_desc(q_at + t * C::kTile + off), sw128_desc(k_at + st * C::kTile + off), id_s,
-                       s > 0 ? 1u : 0u);
-            }
-            tc_commit(&bars.s_full[t]);
-        };
-        bool ok = mbar_wait(&bars.q_full, 0) && mbar_wait(&bars.k_full[0], 0);
-        if (ok) {
-            tc_fence_after();
-            for (int t = 0; t < ntiles_q; ++t) logits(t, 0);
-            tc_commit(&bars.k_empty[0]);
-        }
-        for (int j = 0; j < tiles && ok; ++j) {
-            const int st = j % kStages, sn = (j + 1) % kStages;
-            ok = mbar_wait(&bars.v_full[st], (j / kStages) & 1);
-            for (int t = 0; t < ntiles_q && ok; ++t) {
-                ok = mbar_wait(&bars.p_full[t], j & 1);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int s = 0; s < kKeys / 16; ++s)
-                    tc_mma_ta(tmem + C::kOCol + t * D, tmem + t * kKeys + 8 * s, mn_desc(v_at + st * C::kTile + 2048 * s), id_o,
-                              j > 0 || s > 0 ? 1u : 0u);
-                if (t == ntiles_q - 1) tc_commit(&bars.v_empty[st]);
-                if (j + 1 == tiles) {
-                    tc_commit(&bars.o_full[t]);
-                    continue;
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = (s >> 2) * kPanel + 32 * (s & 3);
+                    tc_mma(tmem + t * kKeys, sw128_desc(q_at + t * C::kTile + off), sw128_desc(k_at + st * C::kTile + off), id_s,
+                           s > 0 ? 1u : 0u);
                 }
-                if (t == 0) ok = mbar_wait(&bars.k_full[sn], ((j + 1) / kStages) & 1);
-                if (!ok) break;
+                tc_commit(&bars.s_full[t]);
+            };
+            bool ok = mbar_wait(&bars.q_full, 0) && mbar_wait(&bars.k_full[0], 0);
+            if (ok) {
                 tc_fence_after();
-                logits(t, sn);
+                for (int t = 0; t < ntiles_q; ++t) logits(t, 0);
+                tc_commit(&bars.k_empty[0]);
             }
-            if (ok && j + 1 < tiles) tc_commit(&bars.k_empty[sn]);
-        }
-        if (!ok) {
-            // every MMA issued completes before tensor memory is freed
-            report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
-            tc_commit(&bars.drain);
-            mbar_wait_for(&bars.drain, 0, kDrainLimitNs);
+            for (int j = 0; j < tiles && ok; ++j) {
+                const int st = j % kStages, sn = (j + 1) % kStages;
+                ok = mbar_wait(&bars.v_full[st], (j / kStages) & 1);
+                for (int t = 0; t < ntiles_q && ok; ++t) {
+                    ok = mbar_wait(&bars.p_full[t], j & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < kKeys / 16; ++s)
+                        tc_mma_ta(tmem + C::kOCol + t * D, tmem + t * kKeys + 8 * s, mn_desc(v_at + st * C::kTile + 2048 * s), id_o,
+                                  j > 0 || s > 0 ? 1u : 0u);
+                    if (t == ntiles_q - 1) tc_commit(&bars.v_empty[st]);
+                    if (j + 1 == tiles) {
+                        tc_commit(&bars.o_full[t]);
+                        continue;
+                    }
+                    if (t == 0) ok = mbar_wait(&bars.k_full[sn], ((j + 1) / kStages) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    logits(t, sn);
+                }
+                if (ok && j + 1 < tiles) tc_commit(&bars.k_empty[sn]);
+            }
+            if (!ok) {
+                // every MMA issued completes before tensor memory is freed
+                report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+                tc_commit(&bars.drain);
+                mbar_wait_for(&bars.drain, 0, kDrainLimitNs);
+            }
         }
     }
     __syncwarp();
