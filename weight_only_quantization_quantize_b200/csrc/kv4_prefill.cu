@@ -167,7 +167,7 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 // Barriers, in shared memory.
 struct Bars {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2], drain;
+    uint64_t q_full, s_full[2], p_half[2][2], pv_half[2], o_full[2], drain;
 };
 
 template <int N>
@@ -234,7 +234,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
         mbar_init(&bars.drain, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars.s_full[t], 1);
-            mbar_init(&bars.p_full[t], 4);
+            mbar_init(&bars.p_half[t][0], 4);
+            mbar_init(&bars.p_half[t][1], 4);
+            mbar_init(&bars.pv_half[t], 1);
             mbar_init(&bars.o_full[t], 1);
         }
         fence_barrier_init();
@@ -304,50 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 const bool plain = ready && (s_valid[st][0] & s_valid[st][1] & s_valid[st][2] & s_valid[st][3]) == 0xffffffffu && tok + kKeys - 1 <= p_lo && tok > w_hi;
                 const float4 vm4 = *reinterpret_cast<const float4 *>(s_vmax[st]);
                 const float vmax = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
-                bool over = !plain;
-                if (plain) {
-                    // the next 32 logits are on their way while these are worked on
-                    uint32_t x[2][32], pk[kKeys / 2];
-                    uint64_t sum0 = 0, sum1 = 0;
-                    const uint64_t nm = two(-m, -m);
-                    tmem_ld32_start(ts, x[0]);
-                    tmem_arrived(x[0]);
-#pragma unroll
-                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
-                        uint32_t(&y)[32] = x[(c0 / 32) & 1];
-                        if (c0 + 32 < kKeys) tmem_ld32_start(ts + c0 + 32, x[(c0 / 32 + 1) & 1]);
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            const ulonglong2 kf = *reinterpret_cast<const ulonglong2 *>(ks + c0 + c);
-                            const ulonglong2 vf = *reinterpret_cast<const ulonglong2 *>(vs + c0 + c);
-                            const float2 y0 = both(fma2(two(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), kf.x, nm));
-                            const float2 y1 = both(fma2(two(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), kf.y, nm));
-                            const uint64_t e0 = two(ex2(y0.x), ex2(y0.y)), e1 = two(ex2(y1.x), ex2(y1.y));
-                            sum0 = add2(sum0, e0);
-                            sum1 = add2(sum1, e1);
-                            const float2 w0 = both(mul2(e0, vf.x)), w1 = both(mul2(e1, vf.y));
-                            pk[(c0 + c) / 2] = pack2(w0.x, w0.y);
-                            pk[(c0 + c) / 2 + 1] = pack2(w1.x, w1.y);
-                        }
-                        if (c0 + 32 < kKeys) tmem_arrived(x[(c0 / 32 + 1) & 1]);
-                    }
-                    const float2 s2 = both(add2(sum0, sum1));
-                    const float sum = s2.x + s2.y;
-                    over = !(sum * vmax <= kLimit);
-                    over = __any_sync(0xffffffffu, over);
-                    if (!over) {
-                        l += sum;
-#pragma unroll
-                        for (int c = 0; c < kKeys / 2; c += 16) {
-                            uint32_t z[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) z[i] = pk[c + i];
-                            tmem_st16(ts + c, z);
-                        }
-                    }
-                }
-                if (over) {
-                    // with masks: the maximum, the reference, the output rows, the weights; 16 keys at a time
+                // the weights of half h, as far as they are stored, go to the second product
+                auto publish = [&](int h) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.p_half[t][h]);
+                };
+                // Keys h0 .. h0 + 63 with masks: the maximum, the reference, the output
+                // rows, the weights, 16 keys at a time.
+                auto masked_half = [&](int h0) -> bool {
                     // the keys c with lo < tok + c <= pos, of those that are there
                     auto seen16 = [&](int c0) -> uint32_t {
                         const int up = pos - tok - c0, dn = lo - tok - c0;
@@ -357,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                     };
                     float top = -INFINITY;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kKeys; c0 += 16) {
+                    for (int c0 = h0; c0 < h0 + 64; c0 += 16) {
                         uint32_t y[16];
                         tmem_ld16(ts + c0, y);
                         const uint32_t seen = seen16(c0);
@@ -374,8 +342,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                         m = next;
                         l *= f;
                     }
-                    if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
-                        // the earlier tiles' sums: their MMAs came before this tile's logits
+                    if ((j > 0 || h0 > 0) && __any_sync(0xffffffffu, f != 1.0f)) {
+                        // the sums so far: those of earlier tiles were complete before this
+                        // tile's logits, the first half's are waited for
+                        if (h0 > 0) {
+                            if (!__all_sync(0xffffffffu, mbar_wait(&bars.pv_half[t], j & 1))) return false;
+                            tc_fence_after();
+                        }
 #pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 16) {
                             uint32_t o[16];
@@ -386,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                         }
                     }
 #pragma unroll 1
-                    for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                    for (int c0 = h0; c0 < h0 + 64; c0 += 32) {
                         uint32_t z[16];
 #pragma unroll
                         for (int g = 0; g < 32; g += 16) {
@@ -409,15 +382,63 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                         }
                         tmem_st16(ts + c0 / 2, z);  // over logits that have been read
                     }
+                    return true;
+                };
+                // Half the tile at a time: the second product starts on the first 64
+                // weights while the others are computed.
+                uint32_t x[2][32];
+                if (plain) tmem_ld32_start(ts, x[0]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int h0 = 64 * h;
+                    bool over = !plain;
+                    if (plain) {
+                        uint32_t pk[32];
+                        uint64_t sum0 = 0, sum1 = 0;
+                        const uint64_t nm = two(-m, -m);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            // the next 32 logits are on their way while these are worked on
+                            tmem_arrived(x[g]);
+                            if (h0 + 32 * g + 32 < kKeys) tmem_ld32_start(ts + h0 + 32 * g + 32, x[1 - g]);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const int k = h0 + 32 * g + c;
+                                const ulonglong2 kf = *reinterpret_cast<const ulonglong2 *>(ks + k);
+                                const ulonglong2 vf = *reinterpret_cast<const ulonglong2 *>(vs + k);
+                                const float2 y0 = both(fma2(two(__uint_as_float(x[g][c]), __uint_as_float(x[g][c + 1])), kf.x, nm));
+                                const float2 y1 = both(fma2(two(__uint_as_float(x[g][c + 2]), __uint_as_float(x[g][c + 3])), kf.y, nm));
+                                const uint64_t e0 = two(ex2(y0.x), ex2(y0.y)), e1 = two(ex2(y1.x), ex2(y1.y));
+                                sum0 = add2(sum0, e0);
+                                sum1 = add2(sum1, e1);
+                                const float2 w0 = both(mul2(e0, vf.x)), w1 = both(mul2(e1, vf.y));
+                                pk[16 * g + c / 2] = pack2(w0.x, w0.y);
+                                pk[16 * g + c / 2 + 1] = pack2(w1.x, w1.y);
+                            }
+                            if (h == 1 && g == 0) publish(0);  // the first half's weights have arrived by now
+                        }
+                        const float2 s2 = both(add2(sum0, sum1));
+                        const float sum = s2.x + s2.y;
+                        over = __any_sync(0xffffffffu, !(sum * vmax <= kLimit));
+                        if (!over) {
+                            l += sum;
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                uint32_t z[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) z[i] = pk[16 * g + i];
+                                tmem_st16(ts + 32 * h + 16 * g, z);
+                            }
+                        }
+                    } else if (h == 1) {
+                        publish(0);
+                    }
+                    if (over) ok = masked_half(h0) && ok;
                 }
+                publish(1);
+                if (lane == 0) mbar_arrive(&bars.k_empty[st]);
+                if (!ok) break;
                 if (!ready) ready = __all_sync(0xffffffffu, m != -INFINITY);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars.p_full[t]);
-                    mbar_arrive(&bars.k_empty[st]);
-                }
             }
             // -------------------------------------------------------- output
             if (tiles > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_full[t], 0));
@@ -579,13 +600,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 const int st = j % kStages, sn = (j + 1) % kStages;
                 ok = mbar_wait(&bars.v_full[st], (j / kStages) & 1);
                 for (int t = 0; t < ntiles_q && ok; ++t) {
-                    ok = mbar_wait(&bars.p_full[t], j & 1);
-                    if (!ok) break;
-                    tc_fence_after();
 #pragma unroll
-                    for (int s = 0; s < kKeys / 16; ++s)
-                        tc_mma_ta(tmem + C::kOCol + t * D, tmem + t * kKeys + 8 * s, mn_desc(v_at + st * C::kTile + 2048 * s), id_o,
-                                  j > 0 || s > 0 ? 1u : 0u);
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && mbar_wait(&bars.p_half[t][h], j & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int s = kKeys / 32 * h; s < kKeys / 32 * (h + 1); ++s)
+                            tc_mma_ta(tmem + C::kOCol + t * D, tmem + t * kKeys + 8 * s, mn_desc(v_at + st * C::kTile + 2048 * s),
+                                      id_o, j > 0 || s > 0 ? 1u : 0u);
+                        if (h == 0) tc_commit(&bars.pv_half[t]);
+                    }
+                    if (!ok) break;
                     if (t == ntiles_q - 1) tc_commit(&bars.v_empty[st]);
                     if (j + 1 == tiles) {
                         tc_commit(&bars.o_full[t]);
