@@ -19,7 +19,10 @@
 //                      codes straight from global memory (the next tile's are in
 //                      registers while this one is written), into two swizzled
 //                      shared-memory buffers each
-//   warp 12            issues the MMAs (128 x 128 x 16 and 128 x D x 16)
+//   warp 12            issues the MMAs (128 x 128 x 16 and 128 x D x 16), the query
+//                      tiles in turn: that keeps their softmaxes apart (an issuer per
+//                      tile lets them fall into step, 383 -> 394 us for the three
+//                      prompts below); three more warps fill the warpgroup
 // Tensor memory: logits 2 x 128 columns, outputs 2 x D columns.  Values stay in
 // token order [token][channel]: the second product reads them as an MN-major
 // operand, so nothing is transposed.
@@ -29,6 +32,8 @@
 // one could have passed 2^14; only then (or while a row has no reference yet, or
 // under a mask) a warp looks for the maximum, moves the reference, rescales its
 // output rows and computes the weights again.
+#include <type_traits>
+
 #include "awq_kernels.cuh"
 #include "kv4.cuh"
 
@@ -167,7 +172,7 @@ __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.
 // Barriers, in shared memory.
 struct Bars {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t q_full, s_full[2], p_half[2][2], pv_half[2], o_full[2], drain;
+    uint64_t q_full[2], s_full[2], p_half[2][2], pv_half[2], o_full[2], drain;
 };
 
 template <int N>
@@ -230,15 +235,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
             mbar_init(&bars.v_full[i], kUnpackWarps);
             mbar_init(&bars.v_empty[i], 1);                 // MMA commit
         }
-        mbar_init(&bars.q_full, 4 * ntiles_q);
-        mbar_init(&bars.drain, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars.s_full[t], 1);
             mbar_init(&bars.p_half[t][0], 4);
             mbar_init(&bars.p_half[t][1], 4);
             mbar_init(&bars.pv_half[t], 1);
+            mbar_init(&bars.q_full[t], 4);
             mbar_init(&bars.o_full[t], 1);
         }
+        mbar_init(&bars.drain, 1);
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -265,21 +270,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
             const bool in = row < rows;
             const int qi = in ? static_cast<int>(row / p.group) : 0;
             const int qh = head * p.group + (in ? static_cast<int>(row - static_cast<long long>(qi) * p.group) : 0);
-            // the query row into its swizzled tile, channels of each 8 in the
-            // order (0,4),(1,5),(2,6),(3,7) that the unpack gives the keys
+            // The warp's 32 query rows into the swizzled tile, W lanes per row,
+            // channels of each 8 in the order (0,4),(1,5),(2,6),(3,7) that the
+            // unpack gives the keys.
             {
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (q0 + qi) * a.q_stride + static_cast<int64_t>(qh) * D);
-                uint8_t *dst = sq + t * C::kTile + r * 128;
+                const int c = lane % W;
+                uint4 x[W];
 #pragma unroll
-                for (int c = 0; c < W; ++c) {
-                    const uint4 x = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                    const uint4 y = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * kPanel + (((c & 7) ^ (r & 7)) << 4)) = y;
+                for (int i = 0; i < W; ++i) {
+                    const int rr = 32 * (warp & 3) + i * (32 / W) + lane / W;
+                    const long long rw = row0 + t * kRowsTile + rr;
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (rw < rows) {
+                        const int ri = static_cast<int>(rw) / p.group;
+                        const int rh = head * p.group + static_cast<int>(rw) - ri * p.group;
+                        x[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (q0 + ri) * a.q_stride + static_cast<int64_t>(rh) * D) + c);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    const int rr = 32 * (warp & 3) + i * (32 / W) + lane / W;
+                    uint8_t *dst = sq + t * C::kTile + rr * 128 + (c >> 3) * kPanel + (((c & 7) ^ (rr & 7)) << 4);
+                    *reinterpret_cast<uint4 *>(dst) =
+                        make_uint4(__byte_perm(x[i].x, x[i].z, 0x5410), __byte_perm(x[i].x, x[i].z, 0x7632),
+                                   __byte_perm(x[i].y, x[i].w, 0x5410), __byte_perm(x[i].y, x[i].w, 0x7632));
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.q_full);
+                if (lane == 0) mbar_arrive(&bars.q_full[t]);
             }
             const int pos = in ? max(len - nq + qi, -1) : -1;
             const int lo = a.window > 0 ? pos - a.window : -1;
@@ -303,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 tc_fence_after();
                 const float *ks = steps + st * 2 * kKeys, *vs = ks + kKeys;
                 const int tok = (tile0 + j) * kKeys;
-                const bool plain = ready && (s_valid[st][0] & s_valid[st][1] & s_valid[st][2] & s_valid[st][3]) == 0xffffffffu && tok + kKeys - 1 <= p_lo && tok > w_hi;
+                const bool clear = (s_valid[st][0] & s_valid[st][1] & s_valid[st][2] & s_valid[st][3]) == 0xffffffffu && tok + kKeys - 1 <= p_lo && tok > w_hi;
                 const float4 vm4 = *reinterpret_cast<const float4 *>(s_vmax[st]);
                 const float vmax = fmaxf(fmaxf(vm4.x, vm4.y), fmaxf(vm4.z, vm4.w));
                 // the weights of half h, as far as they are stored, go to the second product
@@ -313,22 +331,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars.p_half[t][h]);
                 };
+                // which of the n (16 or 32) keys from tok + c0 on are there and seen: lo < key <= pos
+                auto seen_of = [&](int c0, int n) -> uint32_t {
+                    const int up = pos - tok - c0, dn = lo - tok - c0;
+                    uint32_t seen = up < 0 ? 0u : up >= 31 ? 0xffffffffu : (2u << up) - 1u;
+                    if (dn >= 0) seen &= dn >= 31 ? 0u : ~((2u << dn) - 1u);
+                    return seen & (s_valid[st][c0 / 32] >> (n == 16 ? c0 & 16 : 0));
+                };
                 // Keys h0 .. h0 + 63 with masks: the maximum, the reference, the output
                 // rows, the weights, 16 keys at a time.
                 auto masked_half = [&](int h0) -> bool {
-                    // the keys c with lo < tok + c <= pos, of those that are there
-                    auto seen16 = [&](int c0) -> uint32_t {
-                        const int up = pos - tok - c0, dn = lo - tok - c0;
-                        uint32_t seen = up < 0 ? 0u : up >= 15 ? 0xffffu : (2u << up) - 1u;
-                        if (dn >= 0) seen &= dn >= 15 ? 0u : ~((2u << dn) - 1u);
-                        return seen & (s_valid[st][c0 / 32] >> (c0 & 16));
-                    };
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int c0 = h0; c0 < h0 + 64; c0 += 16) {
                         uint32_t y[16];
                         tmem_ld16(ts + c0, y);
-                        const uint32_t seen = seen16(c0);
+                        const uint32_t seen = seen_of(c0, 16);
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             if ((seen >> c) & 1u) top = fmaxf(top, __uint_as_float(y[c]) * ks[c0 + c]);
@@ -365,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                         for (int g = 0; g < 32; g += 16) {
                             uint32_t y[16];
                             tmem_ld16(ts + c0 + g, y);
-                            const uint32_t seen = seen16(c0 + g);
+                            const uint32_t seen = seen_of(c0 + g, 16);
 #pragma unroll
                             for (int c = 0; c < 16; c += 2) {
                                 float pv[2];
@@ -384,56 +402,82 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                     }
                     return true;
                 };
+                if (!ready && clear) {
+                    // a first reference from the first 16 keys, good enough unless a weight passes the limit
+                    uint32_t y[16];
+                    tmem_ld16(ts, y);
+                    float top = __uint_as_float(y[0]) * ks[0];
+#pragma unroll
+                    for (int c = 1; c < 16; ++c) top = fmaxf(top, __uint_as_float(y[c]) * ks[c]);
+                    if (m == -INFINITY)
+                        m = top + static_cast<float>(static_cast<int>(__float_as_uint(vmax) >> 23) - 126) - kGain;
+                    ready = __all_sync(0xffffffffu, m > -INFINITY);
+                }
                 // Half the tile at a time: the second product starts on the first 64
                 // weights while the others are computed.
                 uint32_t x[2][32];
-                if (plain) tmem_ld32_start(ts, x[0]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                if (ready) tmem_ld32_start(ts, x[0]);
+                // Weights of half h with the reference as it stands; true when one may be too large (then nothing is stored).
+                auto weights = [&](auto mask, int h) -> bool {
+                    constexpr bool MASK = decltype(mask)::value;
                     const int h0 = 64 * h;
-                    bool over = !plain;
-                    if (plain) {
-                        uint32_t pk[32];
-                        uint64_t sum0 = 0, sum1 = 0;
-                        const uint64_t nm = two(-m, -m);
+                    uint32_t pk[32];
+                    uint64_t sum0 = 0, sum1 = 0;
+                    const uint64_t nm = two(-m, -m);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        // the next 32 logits are on their way while these are worked on
+                        tmem_arrived(x[g]);
+                        const uint32_t seen = MASK ? seen_of(h0 + 32 * g, 32) : 0u;
+                        if (h0 + 32 * g + 32 < kKeys) tmem_ld32_start(ts + h0 + 32 * g + 32, x[1 - g]);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const int k = h0 + 32 * g + c;
+                            const ulonglong2 kf = *reinterpret_cast<const ulonglong2 *>(ks + k);
+                            const ulonglong2 vf = *reinterpret_cast<const ulonglong2 *>(vs + k);
+                            float2 y0 = both(fma2(two(__uint_as_float(x[g][c]), __uint_as_float(x[g][c + 1])), kf.x, nm));
+                            float2 y1 = both(fma2(two(__uint_as_float(x[g][c + 2]), __uint_as_float(x[g][c + 3])), kf.y, nm));
+                            if constexpr (MASK) {  // weight 0 (absent keys have codes and steps 0: nothing here is NaN)
+                                y0.x = (seen >> c) & 1u ? y0.x : -INFINITY;
+                                y0.y = (seen >> (c + 1)) & 1u ? y0.y : -INFINITY;
+                                y1.x = (seen >> (c + 2)) & 1u ? y1.x : -INFINITY;
+                                y1.y = (seen >> (c + 3)) & 1u ? y1.y : -INFINITY;
+                            }
+                            const uint64_t e0 = two(ex2(y0.x), ex2(y0.y)), e1 = two(ex2(y1.x), ex2(y1.y));
+                            sum0 = add2(sum0, e0);
+                            sum1 = add2(sum1, e1);
+                            const float2 w0 = both(mul2(e0, vf.x)), w1 = both(mul2(e1, vf.y));
+                            pk[16 * g + c / 2] = pack2(w0.x, w0.y);
+                            pk[16 * g + c / 2 + 1] = pack2(w1.x, w1.y);
+                        }
+                        if (h == 1 && g == 0) publish(0);  // the first half's weights have arrived by now
+                    }
+                    const float2 s2 = both(add2(sum0, sum1));
+                    const float sum = s2.x + s2.y;
+                    const bool over = __any_sync(0xffffffffu, !(sum * vmax <= kLimit));
+                    if (!over) {
+                        l += sum;
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
-                            // the next 32 logits are on their way while these are worked on
-                            tmem_arrived(x[g]);
-                            if (h0 + 32 * g + 32 < kKeys) tmem_ld32_start(ts + h0 + 32 * g + 32, x[1 - g]);
+                            uint32_t z[16];
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const int k = h0 + 32 * g + c;
-                                const ulonglong2 kf = *reinterpret_cast<const ulonglong2 *>(ks + k);
-                                const ulonglong2 vf = *reinterpret_cast<const ulonglong2 *>(vs + k);
-                                const float2 y0 = both(fma2(two(__uint_as_float(x[g][c]), __uint_as_float(x[g][c + 1])), kf.x, nm));
-                                const float2 y1 = both(fma2(two(__uint_as_float(x[g][c + 2]), __uint_as_float(x[g][c + 3])), kf.y, nm));
-                                const uint64_t e0 = two(ex2(y0.x), ex2(y0.y)), e1 = two(ex2(y1.x), ex2(y1.y));
-                                sum0 = add2(sum0, e0);
-                                sum1 = add2(sum1, e1);
-                                const float2 w0 = both(mul2(e0, vf.x)), w1 = both(mul2(e1, vf.y));
-                                pk[16 * g + c / 2] = pack2(w0.x, w0.y);
-                                pk[16 * g + c / 2 + 1] = pack2(w1.x, w1.y);
-                            }
-                            if (h == 1 && g == 0) publish(0);  // the first half's weights have arrived by now
+                            for (int i = 0; i < 16; ++i) z[i] = pk[16 * g + i];
+                            tmem_st16(ts + 32 * h + 16 * g, z);
                         }
-                        const float2 s2 = both(add2(sum0, sum1));
-                        const float sum = s2.x + s2.y;
-                        over = __any_sync(0xffffffffu, !(sum * vmax <= kLimit));
-                        if (!over) {
-                            l += sum;
-#pragma unroll
-                            for (int g = 0; g < 2; ++g) {
-                                uint32_t z[16];
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) z[i] = pk[16 * g + i];
-                                tmem_st16(ts + 32 * h + 16 * g, z);
-                            }
-                        }
-                    } else if (h == 1) {
-                        publish(0);
                     }
-                    if (over) ok = masked_half(h0) && ok;
+                    return over;
+                };
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    bool over = !ready;
+                    if (!ready) {
+                        if (h == 1) publish(0);
+                    } else if (clear) {
+                        over = weights(std::false_type{}, h);
+                    } else {
+                        over = weights(std::true_type{}, h);
+                    }
+                    if (over) ok = masked_half(64 * h) && ok;
                 }
                 publish(1);
                 if (lane == 0) mbar_arrive(&bars.k_empty[st]);
@@ -590,12 +634,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 }
                 tc_commit(&bars.s_full[t]);
             };
-            bool ok = mbar_wait(&bars.q_full, 0) && mbar_wait(&bars.k_full[0], 0);
-            if (ok) {
+            bool ok = mbar_wait(&bars.k_full[0], 0);
+            for (int t = 0; t < ntiles_q && ok; ++t) {
+                ok = mbar_wait(&bars.q_full[t], 0);
+                if (!ok) break;
                 tc_fence_after();
-                for (int t = 0; t < ntiles_q; ++t) logits(t, 0);
-                tc_commit(&bars.k_empty[0]);
+                logits(t, 0);
             }
+            if (ok) tc_commit(&bars.k_empty[0]);
             for (int j = 0; j < tiles && ok; ++j) {
                 const int st = j % kStages, sn = (j + 1) % kStages;
                 ok = mbar_wait(&bars.v_full[st], (j / kStages) & 1);
