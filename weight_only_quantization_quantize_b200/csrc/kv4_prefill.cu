@@ -467,17 +467,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                     }
                     return over;
                 };
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    bool over = !ready;
-                    if (!ready) {
-                        if (h == 1) publish(0);
-                    } else if (clear) {
-                        over = weights(std::false_type{}, h);
-                    } else {
-                        over = weights(std::true_type{}, h);
-                    }
-                    if (over) ok = masked_half(64 * h) && ok;
+                // The usual tile first, in one piece of code; what is left of it (masks, a
+                // weight over the limit, no reference yet) in another, once for both halves.
+                int from = 0;
+                if (ready && clear && !weights(std::false_type{}, 0)) from = weights(std::false_type{}, 1) ? 1 : 2;
+#pragma unroll 1
+                for (int h = from; h < 2; ++h) {
+                    if (!ready && h == 1) publish(0);
+                    // the half that has just failed goes on to its maximum
+                    if (!ready || (clear && h == from) || weights(std::true_type{}, h)) ok = masked_half(64 * h) && ok;
                 }
                 publish(1);
                 if (lane == 0) mbar_arrive(&bars.k_empty[st]);
@@ -624,13 +622,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
         if (warp == kMmaWarp && lane == 0 && tiles > 0) {
             constexpr uint32_t id_s = tc_idesc_f16(kRowsTile, kKeys);
             constexpr uint32_t id_o = tc_idesc_f16(kRowsTile, D) | (1u << 16);  // B is MN-major
-            const uint32_t q_at = smem_u32(sq), k_at = smem_u32(sk), v_at = smem_u32(sv);
+            // Descriptors are made once and moved by adding to their address field: the
+            // issuing thread shares its scheduler with three busy warps, and every
+            // instruction between two MMAs shows.
+            const uint64_t q_desc = sw128_desc(smem_u32(sq)), k_desc = sw128_desc(smem_u32(sk)), v_desc = mn_desc(smem_u32(sv));
             auto logits = [&](int t, int st) {
+                const uint64_t qd = q_desc + t * (C::kTile >> 4), kd = k_desc + st * (C::kTile >> 4);
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t off = (s >> 2) * kPanel + 32 * (s & 3);
-                    tc_mma(tmem + t * kKeys, sw128_desc(q_at + t * C::kTile + off), sw128_desc(k_at + st * C::kTile + off), id_s,
-                           s > 0 ? 1u : 0u);
+                    const uint32_t off = ((s >> 2) * kPanel + 32 * (s & 3)) >> 4;
+                    tc_mma(tmem + t * kKeys, qd + off, kd + off, id_s, s > 0 ? 1u : 0u);
                 }
                 tc_commit(&bars.s_full[t]);
             };
@@ -651,10 +652,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                         ok = ok && mbar_wait(&bars.p_half[t][h], j & 1);
                         if (!ok) break;
                         tc_fence_after();
+                        const uint32_t w = tmem + t * kKeys + 32 * h, to = tmem + C::kOCol + t * D;
+                        const uint64_t vd = v_desc + st * (C::kTile >> 4) + h * (8192 >> 4);
+                        tc_mma_ta(to, w, vd, id_o, j > 0 || h > 0 ? 1u : 0u);
 #pragma unroll
-                        for (int s = kKeys / 32 * h; s < kKeys / 32 * (h + 1); ++s)
-                            tc_mma_ta(tmem + C::kOCol + t * D, tmem + t * kKeys + 8 * s, mn_desc(v_at + st * C::kTile + 2048 * s),
-                                      id_o, j > 0 || s > 0 ? 1u : 0u);
+                        for (int s = 1; s < kKeys / 32; ++s) tc_mma_ta(to, w + 8 * s, vd + s * (2048 >> 4), id_o, 1u);
                         if (h == 0) tc_commit(&bars.pv_half[t]);
                     }
                     if (!ok) break;
