@@ -193,6 +193,21 @@ def _check(code: int, where: str):
         raise AwqError(code, where)
 
 
+_current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
+
+def _call(dev: torch.device, where: str, fn, *args):
+    """One C call on `dev`, which costs a device switch only when another one is current."""
+    if dev.index == _current_device():
+        code = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args)
+    if code != OK:
+        raise AwqError(code, where)
+
+
 def new_status(device) -> torch.Tensor:
     """A zeroed device status word for the calls' dev_status argument."""
     return torch.zeros(1, dtype=torch.int32, device=device)
@@ -482,11 +497,11 @@ def _check_epilogue(N, bias, act, gated, dev):
     return ACTIVATIONS[act], int(bool(gated)), N // 2 if gated else N
 
 
-def _epilogue_workspace(dev, M, K, need):
+def _epilogue_workspace(dev, need):
     """Default workspace of a call: the stream's cached one.  A call that is being captured into a graph gets its
     own (from the graph's memory, its counters zeroed by the graph), because graphs captured on one stream
     may be replayed at the same time on others."""
-    if torch.cuda.is_current_stream_capturing():
+    if _capturing():
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         ws[:32768].zero_()
         return ws
@@ -521,7 +536,7 @@ def w4a16_gemm_epilogue(X, s, Q, scales, zeros, bias=None, act=None, gated=False
     with _on(dev):
         wsz = gemm_workspace_size(M, K, N)
         if workspace is None:
-            workspace = _epilogue_workspace(dev, M, K, wsz)
+            workspace = _epilogue_workspace(dev, wsz)
         else:
             _check_workspace(workspace, wsz, dev)
         _check(lib().awq_w4a16_gemm_epilogue(_ptr(X), _ptr(s), _ptr(Q), _ptr(scales), _ptr(zeros), M, K, N,
@@ -560,6 +575,7 @@ class QuantLinear:
         self.bias, self.act, self.gated = bias, act, bool(gated)
         self._act, self._gate, self.out_features = _check_epilogue(self.N, bias, act, gated, self.device)
         self._plain = bias is None and self._act == 0 and not gated
+        self._bptr = _ptr(bias)
         self._dev_index = self.device.index if self.device.index is not None else torch.cuda.current_device()
         self._lib = lib()
 
@@ -583,20 +599,19 @@ class QuantLinear:
         stream = torch._C._cuda_getCurrentRawStream(self._dev_index)
         wsz = self._lib.awq_w4a16_gemm_workspace_size(M, self.K, self.N)
         plain = self._plain and residual is None
-        if workspace is None:
-            with _on(self.device):
-                workspace = workspace_for(self.device, wsz) if plain else \
-                    _epilogue_workspace(self.device, M, self.K, wsz)
-        else:
+        if workspace is not None:
             _check_workspace(workspace, wsz, self.device)
+        elif plain:
+            workspace = workspace_for(self.device, wsz)
+        else:
+            workspace = _epilogue_workspace(self.device, wsz)
         s, q, sc, z = self._wptrs
+        if not plain:
+            _call(self.device, "awq_w4a16_gemm_epilogue", self._lib.awq_w4a16_gemm_epilogue, X.data_ptr(), s, q, sc, z,
+                  M, self.K, self.N, self._bptr, self._act, self._gate, _ptr(residual), out.data_ptr(),
+                  workspace.data_ptr(), workspace.numel(), _ptr(status), stream)
+            return out
         with _on(self.device):
-            if not plain:
-                _check(self._lib.awq_w4a16_gemm_epilogue(
-                    X.data_ptr(), s, q, sc, z, M, self.K, self.N, _ptr(self.bias), self._act, self._gate,
-                    _ptr(residual), out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status), stream),
-                    "awq_w4a16_gemm_epilogue")
-                return out
             _check(self._lib.awq_w4a16_gemm(X.data_ptr(), s, q, sc, z, M, self.K, self.N, out.data_ptr(),
                                             workspace.data_ptr(), workspace.numel(), _ptr(status), stream),
                    "awq_w4a16_gemm")
@@ -661,6 +676,8 @@ class KV4Pages:
         _need(self.free_pages, torch.int32, (num_pages,), "free_pages", dev)
         _need(self.free_count, torch.int32, (1,), "free_count", dev)
         self._lib = lib()
+        self._state = (self.block_table.data_ptr(), max_pages, self.free_pages.data_ptr(), self.free_count.data_ptr(),
+                       num_pages)
 
     def reserve(self, new_lens, total, next_lens=None, next_free=None, out=None, status=None):
         """Pages and slots for new_lens[b] new tokens of each request b (int32 [max_requests]).
@@ -684,8 +701,7 @@ class KV4Pages:
             _match(next_free, torch.int32, (1,), "next_free", dev)
         if out is None:
             slots = torch.empty(total, dtype=torch.int64, device=dev)
-            ints = torch.empty(total + B + 1, dtype=torch.int32, device=dev)
-            positions, cu = ints[:total], ints[total:]
+            positions, cu = self.lens.new_empty(total), self.lens.new_empty(B + 1)
         else:
             slots, positions, cu = out
             _match(slots, torch.int64, (total,), "slots", dev)
@@ -693,12 +709,9 @@ class KV4Pages:
             _match(cu, torch.int32, (B + 1,), "cu", dev)
         if status is not None:
             _need_status(status, dev)
-        with _on(dev):
-            _check(self._lib.awq_kv4_reserve(
-                new_lens.data_ptr(), self.lens.data_ptr(), B, self.page_size, self.block_table.data_ptr(),
-                self.max_pages, self.free_pages.data_ptr(), self.free_count.data_ptr(), self.num_pages, total,
-                slots.data_ptr(), positions.data_ptr(), cu.data_ptr(), next_lens.data_ptr(), next_free.data_ptr(),
-                _ptr(status), _raw_stream(dev)), "awq_kv4_reserve")
+        _call(dev, "awq_kv4_reserve", self._lib.awq_kv4_reserve, new_lens.data_ptr(), self.lens.data_ptr(), B,
+              self.page_size, *self._state, total, slots.data_ptr(), positions.data_ptr(), cu.data_ptr(),
+              next_lens.data_ptr(), next_free.data_ptr(), _ptr(status), _raw_stream(dev))
         return slots, positions, cu
 
     def release(self, done, status=None):
@@ -707,11 +720,8 @@ class KV4Pages:
         _match(done, torch.int32, (self.max_requests,), "done", dev)
         if status is not None:
             _need_status(status, dev)
-        with _on(dev):
-            _check(self._lib.awq_kv4_release(
-                done.data_ptr(), self.lens.data_ptr(), self.max_requests, self.page_size,
-                self.block_table.data_ptr(), self.max_pages, self.free_pages.data_ptr(), self.free_count.data_ptr(),
-                self.num_pages, _ptr(status), _raw_stream(dev)), "awq_kv4_release")
+        _call(dev, "awq_kv4_release", self._lib.awq_kv4_release, done.data_ptr(), self.lens.data_ptr(),
+              self.max_requests, self.page_size, *self._state, _ptr(status), _raw_stream(dev))
 
 
 class KV4Cache:
@@ -729,6 +739,10 @@ class KV4Cache:
         _need(self.data, torch.uint8, shape, "data", pages.device)
         self._lib = lib()
         self._workspace_size = int(self._lib.awq_kv4_attention_workspace_size(head_dim))
+        # the cache as the store's and load's calls and as the attention's call name it
+        self._place = (kv_heads, head_dim, self.data.data_ptr(), pages.num_pages, pages.page_size)
+        self._read = (self.data.data_ptr(), pages.num_pages, pages.page_size, kv_heads, head_dim,
+                      pages.block_table.data_ptr(), pages.max_pages, pages.lens.data_ptr())
 
     def _rows(self, x, name):
         """(T, row stride) of keys or values [T, kv_heads, head_dim] or [T, kv_heads * head_dim], rows apart by any
@@ -766,22 +780,19 @@ class KV4Cache:
             _need_status(status, dev)
         if T == 0:
             return
-        with _on(dev):
-            _check(self._lib.awq_kv4_append(
-                k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, self.kv_heads, self.head_dim,
-                self.data.data_ptr(), self.pages.num_pages, self.pages.page_size, _ptr(status), _raw_stream(dev)),
-                "awq_kv4_append")
+        _call(dev, "awq_kv4_append", self._lib.awq_kv4_append, k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T,
+              *self._place, _ptr(status), _raw_stream(dev))
 
     def load(self, slots, out=None, status=None):
         """The stored keys and values of slots (int64 [T]): (k, v) float16 [T, kv_heads, head_dim]; zeros for a negative
         slot."""
         dev = self.pages.device
-        _match(slots, torch.int64, (slots.shape[0] if isinstance(slots, torch.Tensor) and slots.dim() == 1 else None,),
-               "slots", dev)
-        T = slots.shape[0]
+        T = slots.numel() if isinstance(slots, torch.Tensor) else 0
+        _match(slots, torch.int64, (T,), "slots", dev)
         shape = (T, self.kv_heads, self.head_dim)
         if out is None:
-            k, v = torch.empty((2, *shape), dtype=torch.float16, device=dev)
+            k = torch.empty(shape, dtype=torch.float16, device=dev)
+            v = torch.empty(shape, dtype=torch.float16, device=dev)
         else:
             k, v = out
             _match(k, torch.float16, shape, "k", dev)
@@ -790,10 +801,8 @@ class KV4Cache:
             _need_status(status, dev)
         if T == 0:
             return k, v
-        with _on(dev):
-            _check(self._lib.awq_kv4_load(
-                slots.data_ptr(), T, self.kv_heads, self.head_dim, self.data.data_ptr(), self.pages.num_pages,
-                self.pages.page_size, k.data_ptr(), v.data_ptr(), _ptr(status), _raw_stream(dev)), "awq_kv4_load")
+        _call(dev, "awq_kv4_load", self._lib.awq_kv4_load, slots.data_ptr(), T, *self._place, k.data_ptr(), v.data_ptr(),
+              _ptr(status), _raw_stream(dev))
         return k, v
 
     def attention(self, q, cu=None, max_new=1, scale=None, window=0, out=None, status=None, workspace=None):
@@ -830,19 +839,16 @@ class KV4Cache:
             _need_status(status, dev)
         if T == 0:
             return out
-        with _on(dev):
-            if workspace is None:
-                if torch.cuda.is_current_stream_capturing():
-                    workspace = torch.empty(self._workspace_size, dtype=torch.uint8, device=dev)
-                else:
-                    workspace = _kv4_workspace(dev, self._workspace_size)
-            else:
-                _check_workspace(workspace, self._workspace_size, dev)
-            _check(self._lib.awq_kv4_attention(
-                q.data_ptr(), st[0] if T > 1 else H * D, T, H, self.data.data_ptr(), p.num_pages, p.page_size,
-                self.kv_heads, D, p.block_table.data_ptr(), p.max_pages, p.lens.data_ptr(), _ptr(cu),
-                p.max_requests, max_new, D ** -0.5 if scale is None else scale, window, out.data_ptr(),
-                workspace.data_ptr(), workspace.numel(), _ptr(status), _raw_stream(dev)), "awq_kv4_attention")
+        stream = _raw_stream(dev)
+        if workspace is not None:
+            _check_workspace(workspace, self._workspace_size, dev)
+        elif _capturing():
+            workspace = torch.empty(self._workspace_size, dtype=torch.uint8, device=dev)
+        else:
+            workspace = _kv4_workspace(dev, stream, self._workspace_size)
+        _call(dev, "awq_kv4_attention", self._lib.awq_kv4_attention, q.data_ptr(), st[0] if T > 1 else H * D, T, H,
+              *self._read, _ptr(cu), p.max_requests, max_new, D ** -0.5 if scale is None else scale, window,
+              out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status), stream)
         return out
 
 
@@ -855,8 +861,8 @@ def kv4_attention_workspace_size(head_dim: int) -> int:
 _kv4_workspaces: dict = {}
 
 
-def _kv4_workspace(device: torch.device, nbytes: int) -> torch.Tensor:
-    key = (device.index, _raw_stream(device))
+def _kv4_workspace(device: torch.device, stream: int, nbytes: int) -> torch.Tensor:
+    key = (device.index, stream)
     ws = _kv4_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)

@@ -66,8 +66,12 @@ struct Cfg {
     static constexpr int kCtasPerSm = NT == 1 ? 3 : 2;
 };
 
+// What the joining kernel has to know of an item that a CTA begins and others go on with.
 struct Desc {
-    int count, b, item, pad;  // CTAs that hold a part of the item this CTA begins; 0: none
+    int count;      // CTAs that hold a part of it; 0: none
+    int first_row;  // its first row among the request's (queries times heads of the group)
+    int rows;       // of the request
+    int head, q0, pad[3];
 };
 
 struct Params {
@@ -749,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
                     const uint32_t last = u - v + r.units - 1;
                     const uint32_t big = rest * (share + 1);
                     const uint32_t cl = last < big ? last / (share + 1) : rest + (last - big) / share;
-                    p.desc[cta] = Desc{static_cast<int>(cl - c) + 1, b, item, 0};
+                    p.desc[cta] = Desc{static_cast<int>(cl - c) + 1, rb * C::kRows, r.nq * p.group, head, r.q0, {0, 0, 0}};
                 }
             }
         }
@@ -779,14 +783,27 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p)
     const Desc d = p.desc[cta];
     if (d.count == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const Request r = request_at<ROWS>(p, d.b);
-    const int heads = p.a.cache.heads;
-    const int rb = d.item / heads, head = d.item - rb * heads;
     const int col = static_cast<int>(blockIdx.y) * kWarps + warp;
-    const int row = rb * ROWS + col;
-    if (row >= r.nq * p.group) return;
+    const int row = d.first_row + col;
+    if (row >= d.rows) return;
     // part 0 is in the first CTA's second slot, part i in CTA c + i's first
     auto slot = [&](int i) { return (2 * static_cast<size_t>(cta + i) + (i == 0 ? 1 : 0)) * ROWS + col; };
+    auto part = [&](int i, float (&x)[E]) {
+        const float *src = p.part + slot(i) * D + E * lane;
+        if constexpr (E == 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(src);
+            x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+        } else {
+            const float2 y = *reinterpret_cast<const float2 *>(src);
+            x[0] = y.x; x[1] = y.y;
+        }
+    };
+    // the first parts are on their way while the maximum is taken
+    constexpr int kAhead = 8;
+    float ahead[kAhead][E];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (i < d.count) part(i, ahead[i]);
     float top = -INFINITY;
     for (int i = lane; i < d.count; i += 32) top = fmaxf(top, p.ml[slot(i)].x);
 #pragma unroll
@@ -794,23 +811,25 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Params p)
     float l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < d.count; ++i) {
+    auto join = [&](int i, const float (&x)[E]) {
         const float2 ml = p.ml[slot(i)];
         const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
         l += ml.y * f;
-        const float *src = p.part + slot(i) * D + E * lane;
-        if constexpr (E == 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(src);
-            o[0] += x.x * f; o[1] += x.y * f; o[2] += x.z * f; o[3] += x.w * f;
-        } else {
-            const float2 x = *reinterpret_cast<const float2 *>(src);
-            o[0] += x.x * f; o[1] += x.y * f;
-        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += x[e] * f;
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (i < d.count) join(i, ahead[i]);
+#pragma unroll 4
+    for (int i = kAhead; i < d.count; ++i) {
+        float x[E];
+        part(i, x);
+        join(i, x);
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     const int i = row / p.group;
-    __half *dst = p.a.out + (static_cast<int64_t>(r.q0 + i) * p.a.q_heads + head * p.group + row - i * p.group) * D + E * lane;
+    __half *dst = p.a.out + (static_cast<int64_t>(d.q0 + i) * p.a.q_heads + d.head * p.group + row - i * p.group) * D + E * lane;
     if constexpr (E == 4)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
     else

@@ -263,10 +263,15 @@ cudaError_t launch_kv4_reserve(const int32_t *new_lens, const int32_t *lens, int
     // a CTA for each four tokens per thread, up to the portable cluster size
     int ctas = 1;
     while (ctas < 8 && static_cast<int64_t>(ctas) * kThreads * 4 < T) ctas *= 2;
+    const size_t smem = sizeof(int32_t) * (3 * static_cast<size_t>(B) + 2);
+    if (ctas == 1) {  // a cluster of its own
+        reserve_kernel<<<1, kThreads, smem, st>>>(prm);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(int32_t) * (3 * static_cast<size_t>(B) + 2);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
