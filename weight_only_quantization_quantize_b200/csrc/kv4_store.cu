@@ -22,6 +22,7 @@ namespace awq {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTokens = 4;  // per lane group, their loads in flight together
 
 struct StoreParams {
     Kv4Cache c;
@@ -45,78 +46,101 @@ __device__ __forceinline__ uint8_t *block_of(const Kv4Cache &c, int64_t slot, in
     return c.data + block * kv4_block_bytes(c.D);
 }
 
-// One head row of D = 8 LG channels on LG neighbouring lanes: the lane's packed
-// word, and on every lane the row's (step, zero point) word.
+// (min x, min -x) of a lane's 8 channels, and through LG neighbouring lanes of
+// the row; *bad becomes NaN when one is NaN or infinite.
 template <int LG>
-__device__ __forceinline__ uint32_t quantize_row(uint4 x, uint32_t *meta, bool *nonfinite)
+__device__ __forceinline__ __half2 row_extremes(const uint32_t (&w)[4], __half2 *bad)
 {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     __half2 mn = bits2h(w[0]), mx = mn;
-    bool bad = false;
+    const __half2 zero = __float2half2_rn(0.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         mn = __hmin2(mn, bits2h(w[i]));
         mx = __hmax2(mx, bits2h(w[i]));
-        bad |= (w[i] & 0x7C00u) == 0x7C00u || (w[i] & 0x7C000000u) == 0x7C000000u;
+        *bad = __hfma2(bits2h(w[i]), zero, *bad);
     }
-    // (min x, min -x), one packed exchange per step
     __half2 e = __halves2half2(__hmin(__low2half(mn), __high2half(mn)), __hneg(__hmax(__low2half(mx), __high2half(mx))));
 #pragma unroll
     for (int d = 1; d < LG; d *= 2) e = __hmin2(e, bits2h(__shfl_xor_sync(0xffffffffu, h2bits(e), d)));
+    return e;
+}
+
+// The grid of a row from its extremes: step and zero point as they are stored,
+// and 1 / step.
+__device__ __forceinline__ uint32_t row_grid(__half2 e, float *inv)
+{
     const float lo = fminf(__low2float(e), 0.0f);
     const float hi = -fminf(__high2float(e), 0.0f);
     const __half step = __float2half_rn(__fdiv_rn(fmaxf(__fsub_rn(hi, lo), 1e-5f), 15.0f));
     const float s = __half2float(step);
-    const float inv = __fdiv_rn(1.0f, s);
+    *inv = __frcp_rn(s);
     const float z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
+    return static_cast<uint32_t>(__half_as_ushort(step)) | (static_cast<uint32_t>(z) << 16);
+}
+
+// A lane's packed word.  Adding 1.5 * 2^23 rounds a float to an integer, ties to
+// even, and leaves it in the low bits: no conversion instructions, whose
+// throughput would bound the kernel.
+__device__ __forceinline__ uint32_t row_codes(const uint32_t (&w)[4], uint32_t meta, float inv)
+{
+    const int z = static_cast<int>(meta >> 16) - 0x4B400000;
     uint32_t out = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(bits2h(w[i]));
-        const float q0 = fminf(fmaxf(rintf(__fmul_rn(f.x, inv)) + z, 0.0f), 15.0f);
-        const float q1 = fminf(fmaxf(rintf(__fmul_rn(f.y, inv)) + z, 0.0f), 15.0f);
-        out |= (static_cast<uint32_t>(q0) | (static_cast<uint32_t>(q1) << 4)) << (8 * i);
+        const int a = __float_as_int(__fadd_rn(__fmul_rn(f.x, inv), 12582912.0f)) + z;
+        const int b = __float_as_int(__fadd_rn(__fmul_rn(f.y, inv), 12582912.0f)) + z;
+        out |= static_cast<uint32_t>(min(max(a, 0), 15)) << (8 * i);
+        out |= static_cast<uint32_t>(min(max(b, 0), 15)) << (8 * i + 4);
     }
-    *meta = static_cast<uint32_t>(__half_as_ushort(step)) | (static_cast<uint32_t>(z) << 16);
-    *nonfinite |= bad;
     return out;
 }
 
-// A lane group handles rows r, r + stride, ...; row = (token, head).
+// blockIdx.y is the head; a lane group takes kTokens tokens, a block's width
+// apart, whose loads are all in flight before the first is used.
 template <int LG>
 __global__ void __launch_bounds__(kThreads) append_kernel(const StoreParams p)
 {
     constexpr int D = 8 * LG;
-    const int sub = static_cast<int>(threadIdx.x) % LG;
-    const int64_t rows = p.T * p.c.heads;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / LG);
+    constexpr int kGroups = kThreads / LG;
+    const int sub = static_cast<int>(threadIdx.x) % LG, head = static_cast<int>(blockIdx.y);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGroups * kTokens) + threadIdx.x / LG;
+    const int64_t end = p.c.num_pages << p.c.page_shift;
     bool nonfinite = false, outside = false;
-    // every lane of a warp runs the same number of turns (the exchanges need all)
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads / LG);
-    for (int64_t r0 = first; r0 < rows; r0 += stride) {
-        const int64_t r = r0 + threadIdx.x / LG;
-        int64_t slot = -1;
-        int head = 0;
-        uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
-        if (r < rows) {
-            const int64_t tok = r / p.c.heads;
-            head = static_cast<int>(r - tok * p.c.heads);
-            slot = p.slots[tok];
-            if (slot >= (p.c.num_pages << p.c.page_shift)) {
-                outside = true;
-                slot = -1;
-            }
-            if (slot >= 0) {
-                kx = *reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride + head * D + 8 * sub);
-                vx = *reinterpret_cast<const uint4 *>(p.v + tok * p.v_stride + head * D + 8 * sub);
-            }
+    int64_t slot[kTokens];
+    uint4 kx[kTokens], vx[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t tok = first + i * kGroups;
+        slot[i] = -1;
+        kx[i] = vx[i] = make_uint4(0, 0, 0, 0);
+        if (tok < p.T) {
+            slot[i] = p.slots[tok];
+            kx[i] = *reinterpret_cast<const uint4 *>(p.k + tok * p.k_stride + head * D + 8 * sub);
+            vx[i] = *reinterpret_cast<const uint4 *>(p.v + tok * p.v_stride + head * D + 8 * sub);
         }
-        uint32_t km, vm;
-        const uint32_t kq = quantize_row<LG>(kx, &km, &nonfinite);
-        const uint32_t vq = quantize_row<LG>(vx, &vm, &nonfinite);
-        if (slot >= 0) {
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        if (slot[i] >= end) {
+            outside = true;
+            slot[i] = -1;
+        }
+        // every lane takes part in the exchanges; a row that is not stored is not judged either
+        const uint32_t kw[4] = {kx[i].x, kx[i].y, kx[i].z, kx[i].w}, vw[4] = {vx[i].x, vx[i].y, vx[i].z, vx[i].w};
+        __half2 bad2 = __float2half2_rn(0.0f);
+        const __half2 ke = row_extremes<LG>(kw, &bad2), ve = row_extremes<LG>(vw, &bad2);
+        // half of the lanes work out the key's grid, half the value's
+        float inv;
+        const uint32_t meta = row_grid(sub < LG / 2 ? ke : ve, &inv);
+        const uint32_t km = __shfl_sync(0xffffffffu, meta, 0, LG), vm = __shfl_sync(0xffffffffu, meta, LG / 2, LG);
+        const float ki = __shfl_sync(0xffffffffu, inv, 0, LG), vi = __shfl_sync(0xffffffffu, inv, LG / 2, LG);
+        const uint32_t kq = row_codes(kw, km, ki), vq = row_codes(vw, vm, vi);
+        const bool bad = __hisnan(__low2half(bad2)) || __hisnan(__high2half(bad2));
+        if (slot[i] >= 0) {
+            nonfinite |= bad;
             int row;
-            uint8_t *b = block_of(p.c, slot, head, &row);
+            uint8_t *b = block_of(p.c, slot[i], head, &row);
             reinterpret_cast<uint32_t *>(b + row * (D / 2))[sub] = kq;
             reinterpret_cast<uint32_t *>(b + 8 * D + row * (D / 2))[sub] = vq;
             if (sub < 2) reinterpret_cast<uint32_t *>(b + 16 * D + 64 * sub)[row] = sub ? vm : km;
@@ -154,36 +178,47 @@ template <int LG>
 __global__ void __launch_bounds__(kThreads) load_kernel(const LoadParams p)
 {
     constexpr int D = 8 * LG;
-    const int sub = static_cast<int>(threadIdx.x) % LG;
-    const int64_t rows = p.T * p.c.heads;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / LG);
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kThreads / LG) + threadIdx.x / LG; r < rows; r += stride) {
-        const int64_t tok = r / p.c.heads;
-        const int head = static_cast<int>(r - tok * p.c.heads);
-        int64_t slot = p.slots[tok];
-        if (slot >= (p.c.num_pages << p.c.page_shift)) {
+    constexpr int kGroups = kThreads / LG;
+    const int sub = static_cast<int>(threadIdx.x) % LG, head = static_cast<int>(blockIdx.y);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kGroups * kTokens) + threadIdx.x / LG;
+    const int64_t end = p.c.num_pages << p.c.page_shift;
+    int64_t slot[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t tok = first + i * kGroups;
+        slot[i] = tok < p.T ? p.slots[tok] : -1;
+        if (slot[i] >= end) {
             report(p.status, AWQ_ERR_RANGE);
-            slot = -1;
+            slot[i] = -1;
         }
-        uint4 ko = make_uint4(0, 0, 0, 0), vo = ko;
-        if (slot >= 0) {
+    }
+    uint32_t kq[kTokens], vq[kTokens], km[kTokens], vm[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        kq[i] = vq[i] = km[i] = vm[i] = 0;  // reads as zeros
+        if (slot[i] >= 0) {
             int row;
-            const uint8_t *b = block_of(p.c, slot, head, &row);
-            const uint32_t kq = reinterpret_cast<const uint32_t *>(b + row * (D / 2))[sub];
-            const uint32_t vq = reinterpret_cast<const uint32_t *>(b + 8 * D + row * (D / 2))[sub];
-            ko = dequant_word(kq, reinterpret_cast<const uint32_t *>(b + 16 * D)[row]);
-            vo = dequant_word(vq, reinterpret_cast<const uint32_t *>(b + 16 * D + 64)[row]);
+            const uint8_t *b = block_of(p.c, slot[i], head, &row);
+            kq[i] = reinterpret_cast<const uint32_t *>(b + row * (D / 2))[sub];
+            vq[i] = reinterpret_cast<const uint32_t *>(b + 8 * D + row * (D / 2))[sub];
+            km[i] = reinterpret_cast<const uint32_t *>(b + 16 * D)[row];
+            vm[i] = reinterpret_cast<const uint32_t *>(b + 16 * D + 64)[row];
         }
-        *reinterpret_cast<uint4 *>(p.k + r * D + 8 * sub) = ko;
-        *reinterpret_cast<uint4 *>(p.v + r * D + 8 * sub) = vo;
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+        const int64_t tok = first + i * kGroups;
+        if (tok >= p.T) break;
+        const int64_t r = tok * p.c.heads + head;
+        *reinterpret_cast<uint4 *>(p.k + r * D + 8 * sub) = dequant_word(kq[i], km[i]);
+        *reinterpret_cast<uint4 *>(p.v + r * D + 8 * sub) = dequant_word(vq[i], vm[i]);
     }
 }
 
-unsigned grid_for(int64_t rows, int lg)
+dim3 grid_for(int64_t T, int heads, int lg)
 {
-    const int64_t per = kThreads / lg;
-    const int64_t blocks = (rows + per - 1) / per;
-    return static_cast<unsigned>(blocks < (1 << 20) ? blocks : (1 << 20));
+    const int64_t per = static_cast<int64_t>(kThreads / lg) * kTokens;
+    return dim3(static_cast<unsigned>((T + per - 1) / per), static_cast<unsigned>(heads));
 }
 
 }  // namespace
@@ -193,9 +228,9 @@ cudaError_t launch_kv4_append(const Kv4Cache &c, const __half *k, int64_t k_stri
 {
     const StoreParams prm{c, k, v, k_stride, v_stride, slots, T, status};
     if (c.D == 128)
-        append_kernel<16><<<grid_for(T * c.heads, 16), kThreads, 0, st>>>(prm);
+        append_kernel<16><<<grid_for(T, c.heads, 16), kThreads, 0, st>>>(prm);
     else
-        append_kernel<8><<<grid_for(T * c.heads, 8), kThreads, 0, st>>>(prm);
+        append_kernel<8><<<grid_for(T, c.heads, 8), kThreads, 0, st>>>(prm);
     return cudaGetLastError();
 }
 
@@ -204,9 +239,9 @@ cudaError_t launch_kv4_load(const Kv4Cache &c, const int64_t *slots, int64_t T, 
 {
     const LoadParams prm{c, slots, k, v, T, status};
     if (c.D == 128)
-        load_kernel<16><<<grid_for(T * c.heads, 16), kThreads, 0, st>>>(prm);
+        load_kernel<16><<<grid_for(T, c.heads, 16), kThreads, 0, st>>>(prm);
     else
-        load_kernel<8><<<grid_for(T * c.heads, 8), kThreads, 0, st>>>(prm);
+        load_kernel<8><<<grid_for(T, c.heads, 8), kThreads, 0, st>>>(prm);
     return cudaGetLastError();
 }
 
