@@ -88,10 +88,11 @@ __device__ __forceinline__ uint32_t row_codes(const uint32_t (&w)[4], uint32_t m
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(bits2h(w[i]));
-        const int a = __float_as_int(__fadd_rn(__fmul_rn(f.x, inv), 12582912.0f)) + z;
-        const int b = __float_as_int(__fadd_rn(__fmul_rn(f.y, inv), 12582912.0f)) + z;
-        out |= static_cast<uint32_t>(min(max(a, 0), 15)) << (8 * i);
-        out |= static_cast<uint32_t>(min(max(b, 0), 15)) << (8 * i + 4);
+        // max(min(rounded + z, 15), 0), one instruction
+        const int a = __viaddmin_s32_relu(__float_as_int(__fadd_rn(__fmul_rn(f.x, inv), 12582912.0f)), z, 15);
+        const int b = __viaddmin_s32_relu(__float_as_int(__fadd_rn(__fmul_rn(f.y, inv), 12582912.0f)), z, 15);
+        out += static_cast<uint32_t>(a) << (8 * i);
+        out += static_cast<uint32_t>(b) << (8 * i + 4);
     }
     return out;
 }
