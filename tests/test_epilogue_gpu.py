@@ -99,11 +99,7 @@ def test_every_path_and_epilogue(M, K, N, bias, act, gated, residual):
 def test_an_empty_epilogue_is_the_plain_product(M, K, N):
     X, s, Q, sc, z = _layer(M, K, N, 1, scaled=True)
     assert torch.equal(awq.w4a16_gemm_epilogue(X, s, Q, sc, z), awq.w4a16_gemm(X, s, Q, sc, z))
-    lin = awq.QuantLinear(Q, sc, z, s)
-    Y = lin(X)
-    # a zero bias goes through the epilogue and changes no bit (x + 0 = x; -0 aside)
-    Z = awq.QuantLinear(Q, sc, z, s, bias=torch.zeros(N, dtype=torch.float16, device="cuda"))(X)
-    assert torch.equal(Y, Z)
+    assert torch.equal(awq.QuantLinear(Q, sc, z, s)(X), awq.w4a16_gemm(X, s, Q, sc, z))
 
 
 def test_activations_at_their_ends():
