@@ -493,8 +493,9 @@ AWQ_API awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_he
  *   AWQ_KV4_MAX_REQUESTS; 1 <= T, max_new < 2^31; max_pages * page_size < 2^31;
  *   B * kv_heads * ceil(max_new * q_heads / kv_heads / 8) * (max_pages * page_size /
  *   32 + 4) < 2^32
- * The result depends on the number of SMs (which fixes the order of sums),
- * never on timing: the same call gives the same bits.
+ * The result depends on the number of SMs and on the bounds max_new, max_pages
+ * and T (which choose the kernel and the order of sums), never on timing: the
+ * same call gives the same bits.
  * Device errors: AWQ_ERR_RANGE (a length above max_pages * page_size or negative:
  * clamped; a page outside the cache: its tokens are not seen; offsets outside
  * 0..T or a request with more than max_new queries: its rows are not written),

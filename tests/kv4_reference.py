@@ -100,7 +100,7 @@ def attention(q, cache, table, lens, cu, page, scale, window=0):
             o = w @ v[:, h]
             av = w @ v[:, h].abs()
             a15 = (w * (15 * vs[:, h])).sum(-1, keepdim=True)
-            eps_s = 2.0 ** -19 * scale * 15 * ks[:, h].max() * qh.abs().sum(-1, keepdim=True)
+            eps_s = 2.0 ** -19 * abs(scale) * 15 * ks[:, h].max() * qh.abs().sum(-1, keepdim=True)
             bd = 2.0 ** -11 * (o.abs() + av) * 1.01 + (n / 16 + 32) * 2.0 ** -23 * a15 + 2 * eps_s * av + 2.0 ** -24
             o[:, ~some] = 0
             out[a:e, h * g: (h + 1) * g] = o.transpose(0, 1)

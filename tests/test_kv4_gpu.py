@@ -414,3 +414,103 @@ def test_arguments_are_checked_before_any_launch():
         awq.KV4Cache(p, 2, 64, data=torch.zeros(2, 2, 8, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("D,Hk,group,page", [(128, 1, 4, 16), (64, 2, 3, 64)])
+@pytest.mark.parametrize("lens,new,window", [([3000, 1500, 70, 5], [70, 33, 70, 5], 0), ([3000, 1500, 70, 5], [70, 33, 70, 5], 700),
+                                             ([4097], [300], 0), ([200], [200], 64)])
+def test_prompts_whose_keys_are_split(D, Hk, group, page, lens, new, window):
+    # a wide table and few row blocks: the keys go to several CTAs, some of which see none
+    p, c, table = _filled(lens, Hk, D, page, seed=sum(lens) + D, max_pages=-(-8192 // page))
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = _rows(cu[-1] + 2, Hk * group, D, 13)
+    a = _check_attention(c, table, q, cu, lens, max(new), window=window)
+    b = _check_attention(c, table, q, cu, lens, max(new), window=window)
+    assert torch.equal(a, b)
+
+
+def test_prompt_rows_with_extreme_steps_and_scales():
+    # value steps six decades apart, logits that keep growing, and both signs of the scale
+    H, D, page, n = 1, 128, 16, 700
+    p, c, table = _filled([n], H, D, page, seed=31)
+    g = torch.Generator().manual_seed(1)
+    k = torch.randn(n, H, D, generator=g) * torch.linspace(0.02, 3.0, n)[:, None, None]
+    v = torch.randn(n, H, D, generator=g) * (10.0 ** (torch.arange(n) % 7 - 3))[:, None, None]
+    pos = torch.arange(n)
+    c.append(k.half().cuda(), v.half().cuda(), (table[0].long()[pos // page] * page + pos % page).cuda())
+    for m in (1, 20, 120, 700):
+        q = torch.randn(m, 4, D, generator=g).half()
+        for scale in (0.088, -0.088, 1.5, 0.0):
+            _check_attention(c, table, q, [0, m], [n], m, scale=scale)
+
+
+def test_stored_zeros_are_attended_to():
+    # slots that were never written (all bytes zero): keys and values of zero, an even average
+    for m in (1, 100):
+        p, c, table = _filled([300], 1, 64, 16, seed=2, poison=False)
+        c.data.zero_()
+        k = _rows(4, 1, 64, 3)
+        at = torch.tensor([17, 100, 150, 299])
+        c.append(k.cuda(), k.cuda(), (table[0].long()[at // 16] * 16 + at % 16).cuda())
+        _check_attention(c, table, _rows(m, 2, 64, 1), [0, m], [300], m)
+
+
+def test_two_caches_at_the_same_time():
+    # calls on two streams, each with its stream's workspace, decode and prompt kernels mixed
+    made = []
+    for i, (lens, new) in enumerate([([900, 4000], [1, 1]), ([600, 333], [600, 200])]):
+        p, c, table = _filled(lens, 2, 128, 32, seed=40 + i)
+        cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+        q = _rows(cu[-1], 8, 128, 41 + i).cuda()
+        want, bound = ref.attention(q.cpu(), _bytes(c.data), table.numpy(), lens, cu, 32, 128 ** -0.5)
+        made.append((c, q, torch.tensor(cu, dtype=torch.int32, device="cuda"), max(new), want, bound, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for o, (c, q, cu, most, _, _, s) in zip(outs, made):
+            with torch.cuda.stream(s):
+                o.append(c.attention(q, cu=cu, max_new=most))
+    torch.cuda.synchronize()
+    for o, (c, q, cu, most, want, bound, s) in zip(outs, made):
+        for x in o:
+            assert bool(((x.cpu().double() - want).abs() <= bound).all()) and torch.equal(x, o[0])
+
+
+def test_captured_step_grows_the_cache():
+    # reserve, store and attention in one graph: each replay adds a token to every request
+    B, Hk, D, page = 3, 2, 64, 16
+    p = awq.KV4Pages(40, page, B, 8)
+    c = awq.KV4Cache(p, Hk, D)
+    st = awq.new_status("cuda")
+    new = torch.ones(B, dtype=torch.int32, device="cuda")
+    qkv = torch.zeros(B, (4 + 2 * Hk) * D, dtype=torch.float16, device="cuda")
+    q, k, v = qkv[:, : 4 * D].unflatten(1, (4, D)), qkv[:, 4 * D: (4 + Hk) * D], qkv[:, (4 + Hk) * D:]
+    out = torch.zeros(B, 4, D, dtype=torch.float16, device="cuda")
+
+    def step():
+        slots, _, _ = p.reserve(new, B, status=st)
+        c.append(k, v, slots, status=st)
+        c.attention(q, out=out, status=st)
+    step()   # outside the graph first
+    p.release(new)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    tokens = []
+    for i in range(37):
+        x = _rows(B, 1, qkv.shape[1], 50 + i)[:, 0]
+        tokens.append(x)
+        qkv.copy_(x)
+        g.replay()
+        awq.raise_on_status(st)
+        if i in (0, 15, 16, 36):
+            assert p.lens.tolist() == [i + 1] * B and int(p.free_count) == 40 - B * -(-(i + 1) // page)
+            table = p.block_table.cpu().numpy()
+            cache = np.zeros_like(_bytes(c.data))
+            for j, tk in enumerate(tokens):
+                slots = [int(table[b, j // page]) * page + j % page for b in range(B)]
+                ref.store(cache, tk[:, 4 * D: (4 + Hk) * D].reshape(B, Hk, D).numpy(),
+                          tk[:, (4 + Hk) * D:].reshape(B, Hk, D).numpy(), slots, page)
+            want, bound = ref.attention(x[:, : 4 * D].reshape(B, 4, D), cache, table, [i + 1] * B, [0, 1, 2, 3], page, D ** -0.5)
+            assert bool(((out.cpu().double() - want).abs() <= bound).all())

@@ -607,7 +607,12 @@ awq::Kv4Cache kv4_cache(const uint8_t *data, int64_t kv_heads, int64_t D, int64_
                          page_shift_of(page_size)};
 }
 
-constexpr int64_t kPrefillRows = 64;
+// Query rows per key/value head and request from which the prompt kernel takes
+// over.  The split kernel covers 16 rows per pass over the cache, the prompt
+// kernel 256, at a higher fixed cost.  Measured, split against prompt kernel, in
+// us: 32 rows 39 / 47 (1 x 32000 keys), 47 / 77 (16 x 4000); 64 rows 57 / 49 and
+// 156 / 100 (32 x 4000); 128 rows 94 / 51.
+constexpr int64_t kPrefillRows = 48;
 
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 }  // namespace
@@ -698,7 +703,9 @@ awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_heads, int
 
 size_t awq_kv4_attention_workspace_size(int64_t D)
 {
-    return D == 64 || D == 128 ? awq::kv4_attend_workspace(static_cast<int>(D)) : 0;
+    if (D != 64 && D != 128) return 0;
+    const size_t a = awq::kv4_attend_workspace(static_cast<int>(D)), p = awq::kv4_prefill_workspace(static_cast<int>(D));
+    return a > p ? a : p;
 }
 
 awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, int64_t q_heads, const uint8_t *cache,
@@ -738,7 +745,7 @@ awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, i
     a.scale = scale;
     a.status = dev_status;
     if (max_new * (q_heads / kv_heads) > kPrefillRows)
-        return from_cuda(awq::launch_kv4_prefill(a, static_cast<cudaStream_t>(stream)));
+        return from_cuda(awq::launch_kv4_prefill(a, workspace, sms, static_cast<cudaStream_t>(stream)));
     return from_cuda(awq::launch_kv4_attend(a, workspace, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -70,6 +70,7 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, void *ws, int num_sms, cud
 
 // kv4_prefill.cu -- many query rows per key/value head: tcgen05
 cudaError_t configure_kv4_prefill();
-cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, cudaStream_t st);
+size_t kv4_prefill_workspace(int D);
+cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, void *ws, int num_sms, cudaStream_t st);
 
 }  // namespace awq

@@ -29,7 +29,7 @@
 //
 // The row maximum is not computed: the weights use a standing reference.  The sum
 // of a tile's weights, times the largest value step of the tile, tells whether
-// one could have passed 2^14; only then (or while a row has no reference yet, or
+// one could have left binary16; only then (or while a row has no reference yet, or
 // under a mask) a warp looks for the maximum, moves the reference, rescales its
 // output rows and computes the weights again.
 #include <type_traits>
@@ -51,9 +51,11 @@ constexpr int kThreads = 512;            // the issuer's warpgroup has three idl
 // registers per thread of each warpgroup; the launch gives 128 to every thread
 constexpr int kSoftmaxRegs = 168, kUnpackRegs = 104, kIssueRegs = 72;
 static_assert(256 * kSoftmaxRegs + 128 * kUnpackRegs + 128 * kIssueRegs <= kThreads * 128, "register shares");
-constexpr float kGain = 6.0f;       // log2 of the largest weight, steps included, after an update
-constexpr float kSlack = 13.0f;     // log2 of the one that asks for the next
-constexpr float kLimit = 16384.0f;  // a tile's weights that add up to less hold none above
+// log2 of the largest weight, steps included, after an update; of the one that
+// asks for the next; and the sum of half a tile's weights below which none can
+// be above it (binary16 ends at 65504).  A higher gain trips over the sums: 9
+// took the three prompts from 335 to 452 us.
+constexpr float kGain = 6.0f, kSlack = 15.0f, kLimit = 46340.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPanel = kKeys * 128;      // bytes of 128 rows x 64 binary16, 128-byte swizzle
 
@@ -70,6 +72,10 @@ struct Cfg {
 struct Params {
     Kv4AttendArgs a;
     int group;
+    int blocks;    // row blocks of a request and head at most
+    int splits;    // parts of every row block's keys, one CTA each
+    float2 *ml;    // splits > 1, [row block][split][256]: (reference, sum) of a row
+    float *part;   // [row block][split][256][D]: its numerators
     UnpackConsts uk;
 };
 
@@ -175,6 +181,12 @@ struct Bars {
     uint64_t q_full[2], s_full[2], p_half[2][2], pv_half[2], o_full[2], drain;
 };
 
+// An upper bound of log2(step), at most 1 above it (steps are normal floats, or 0).
+__device__ __forceinline__ float step_log2(float step)
+{
+    return static_cast<float>(static_cast<int>(__float_as_uint(step) >> 23) - 126);
+}
+
 template <int N>
 __device__ __forceinline__ void more_registers()
 {
@@ -207,14 +219,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
     // ---------------------------------------------------------------- this CTA's rows and keys
     // later row blocks see more keys: they come first
     const int b = static_cast<int>(blockIdx.z), head = static_cast<int>(blockIdx.y);
-    const int rb = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+    const int rb = p.blocks - 1 - static_cast<int>(blockIdx.x) / p.splits;
+    const int split = static_cast<int>(blockIdx.x) % p.splits;
     const long long most = static_cast<long long>(a.tab.max_pages) << a.cache.page_shift;
     int len = a.tab.lens[b];
     const int q0 = a.tab.cu ? a.tab.cu[b] : b;
     const long long q1 = a.tab.cu ? a.tab.cu[b + 1] : b + 1;
     const long long nql = q1 - q0;
     const bool bad_rows = q0 < 0 || nql < 0 || q1 > a.T || nql > a.max_new;
-    if (threadIdx.x == 0 && rb == 0 && head == 0 && (bad_rows || len < 0 || len > most)) report(a.status, AWQ_ERR_RANGE);
+    if (threadIdx.x == 0 && rb == 0 && head == 0 && split == 0 && (bad_rows || len < 0 || len > most)) report(a.status, AWQ_ERR_RANGE);
     const int nq = bad_rows ? 0 : static_cast<int>(nql);
     len = len < 0 ? 0 : len > most ? static_cast<int>(most) : len;
     const long long rows = static_cast<long long>(nq) * p.group;
@@ -225,8 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
     const int pfirst = max(len - nq + static_cast<int>(row0 / p.group), -1);  // positions; -1: before the first token
     const int plast = max(len - nq + rlast / p.group, -1);
     const int lo_first = a.window > 0 ? max(pfirst - a.window + 1, 0) : 0;
-    const int tile0 = lo_first / kKeys;
-    const int tiles = plast < 0 ? 0 : plast / kKeys + 1 - tile0;
+    // this split's share of the key tiles
+    const int all0 = lo_first / kKeys;
+    const int all = plast < 0 ? 0 : plast / kKeys + 1 - all0;
+    const int share = (all + p.splits - 1) / p.splits;
+    const int tile0 = all0 + min(split * share, all);
+    const int tiles = min(share, all - (tile0 - all0));
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -349,10 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                         const uint32_t seen = seen_of(c0, 16);
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
-                            if ((seen >> c) & 1u) top = fmaxf(top, __uint_as_float(y[c]) * ks[c0 + c]);
+                            if ((seen >> c) & 1u) top = fmaxf(top, fmaf(__uint_as_float(y[c]), ks[c0 + c], step_log2(vs[c0 + c])));
                     }
-                    // an upper bound of the weights' logarithms, steps included
-                    top += static_cast<float>(static_cast<int>(__float_as_uint(vmax) >> 23) - 126);
                     float f = 1.0f;
                     if (top > m + kSlack) {
                         const float next = top - kGain;
@@ -406,11 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                     // a first reference from the first 16 keys, good enough unless a weight passes the limit
                     uint32_t y[16];
                     tmem_ld16(ts, y);
-                    float top = __uint_as_float(y[0]) * ks[0];
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int c = 1; c < 16; ++c) top = fmaxf(top, __uint_as_float(y[c]) * ks[c]);
-                    if (m == -INFINITY)
-                        m = top + static_cast<float>(static_cast<int>(__float_as_uint(vmax) >> 23) - 126) - kGain;
+                    for (int c = 0; c < 16; ++c) top = fmaxf(top, fmaf(__uint_as_float(y[c]), ks[c], step_log2(vs[c])));
+                    if (m == -INFINITY) m = top - kGain;
                     ready = __all_sync(0xffffffffu, m > -INFINITY);
                 }
                 // Half the tile at a time: the second product starts on the first 64
@@ -488,10 +502,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 if (lane == 0) report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
             } else {
                 tc_fence_after();
+                if (p.splits > 1) {
+                    // numerators, reference and sum for the join
+                    const size_t at = ((static_cast<size_t>(b) * gridDim.y + head) * p.blocks + rb) * p.splits + split;
+                    const size_t slot = at * kRowsCta + t * kRowsTile + r;
+                    if (in) p.ml[slot] = make_float2(m, l);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D && tiles > 0; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_start(to + c0, o);
+                        tmem_arrived(o);
+                        if (!in) continue;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8) {
+                            // columns hold channels 0, 4, 1, 5, 2, 6, 3, 7 of each 8
+                            uint4 *dst = reinterpret_cast<uint4 *>(p.part + slot * D + c0 + c);
+                            dst[0] = make_uint4(o[c], o[c + 2], o[c + 4], o[c + 6]);
+                            dst[1] = make_uint4(o[c + 1], o[c + 3], o[c + 5], o[c + 7]);
+                        }
+                    }
+                }
                 const float inv = l > 0.0f ? 1.0f / l : 0.0f;
                 uint4 *dst = reinterpret_cast<uint4 *>(a.out + (static_cast<int64_t>(q0 + qi) * a.q_heads + qh) * D);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = 0; c0 < D && p.splits == 1; c0 += 32) {
                     uint32_t o[32];
                     if (tiles > 0)
                         tmem_ld32(to + c0, o);
@@ -690,7 +724,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
     }
 }
 
+// Joins the splits of a row block, one warp per row, in the order of the splits.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const Params p)
+{
+    constexpr int E = D / 32;
+    pdl_wait();
+    const Kv4AttendArgs &a = p.a;
+    const int b = static_cast<int>(blockIdx.z), head = static_cast<int>(blockIdx.y);
+    const int rb = static_cast<int>(blockIdx.x) / (kRowsCta / 8);
+    const int r = static_cast<int>(blockIdx.x) % (kRowsCta / 8) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int q0 = a.tab.cu ? a.tab.cu[b] : b;
+    const long long q1 = a.tab.cu ? a.tab.cu[b + 1] : b + 1, nq = q1 - q0;
+    if (q0 < 0 || nq < 0 || q1 > a.T || nq > a.max_new) return;
+    const long long row = static_cast<long long>(rb) * kRowsCta + r;
+    if (row >= nq * p.group) return;
+    const size_t first = ((static_cast<size_t>(b) * gridDim.y + head) * p.blocks + rb) * p.splits;
+    auto slot = [&](int s) { return (first + s) * kRowsCta + r; };
+    float top = -INFINITY;
+    for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, p.ml[slot(s)].x);
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    float l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const float2 ml = p.ml[slot(s)];
+        if (ml.x == -INFINITY) continue;  // saw no key: its numerators may not be written
+        const float f = ex2(ml.x - top);
+        l += ml.y * f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += p.part[slot(s) * D + E * lane + e] * f;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const int qi = static_cast<int>(row) / p.group;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (static_cast<int64_t>(q0 + qi) * a.q_heads + head * p.group +
+                                                           static_cast<int>(row) - qi * p.group) * D + E * lane);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack2(o[e] * inv, o[e + 1] * inv);
+}
+
+// Partial results that the workspace holds, 256 rows each.
+constexpr int kMaxParts = 160;
+constexpr size_t kMlBytes = sizeof(float2) * kMaxParts * kRowsCta;
+
 }  // namespace
+
+size_t kv4_prefill_workspace(int D) { return kMlBytes + sizeof(float) * kMaxParts * kRowsCta * static_cast<size_t>(D); }
 
 cudaError_t configure_kv4_prefill()
 {
@@ -701,20 +782,43 @@ cudaError_t configure_kv4_prefill()
                                 static_cast<int>(Cfg<64>::kSmem));
 }
 
-cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, cudaStream_t st)
+cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, void *ws, int num_sms, cudaStream_t st)
 {
     Params prm{};
     prm.a = a;
     prm.group = a.q_heads / a.cache.heads;
     prm.uk = unpack_consts();
-    const int64_t new_rows = a.max_new < a.T ? a.max_new : a.T;
-    const dim3 grid(static_cast<unsigned>((new_rows * prm.group + kRowsCta - 1) / kRowsCta),
-                    static_cast<unsigned>(a.cache.heads), static_cast<unsigned>(a.tab.B));
+    const int64_t new_rows = (a.max_new < a.T ? a.max_new : a.T) * static_cast<int64_t>(prm.group);
+    prm.blocks = static_cast<int>((new_rows + kRowsCta - 1) / kRowsCta);
+    // Few row blocks leave SMs idle: their keys are split until the GPU is full,
+    // into parts of at least four tiles (by the table's width, the only length
+    // known here).
+    const int64_t blocks = static_cast<int64_t>(prm.blocks) * a.cache.heads * a.tab.B;
+    const int sms = num_sms < kMaxParts ? num_sms : kMaxParts;
+    const int64_t by_keys = (static_cast<int64_t>(a.tab.max_pages) << a.cache.page_shift) / (4 * kKeys);
+    int64_t splits = blocks < sms ? sms / blocks : 1;
+    if (splits > by_keys) splits = by_keys < 1 ? 1 : by_keys;
+    prm.splits = static_cast<int>(splits);
+    prm.ml = static_cast<float2 *>(ws);
+    prm.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kMlBytes);
+    const dim3 grid(static_cast<unsigned>(prm.blocks * prm.splits), static_cast<unsigned>(a.cache.heads),
+                    static_cast<unsigned>(a.tab.B));
     if (a.cache.D == 128)
         prefill_kernel<128><<<grid, kThreads, Cfg<128>::kSmem, st>>>(prm);
     else
         prefill_kernel<64><<<grid, kThreads, Cfg<64>::kSmem, st>>>(prm);
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || prm.splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(prm.blocks) * (kRowsCta / 8), grid.y, grid.z);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return a.cache.D == 128 ? cudaLaunchKernelEx(&cfg, join_kernel<128>, prm) : cudaLaunchKernelEx(&cfg, join_kernel<64>, prm);
 }
 
 }  // namespace awq
