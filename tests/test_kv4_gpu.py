@@ -514,3 +514,37 @@ def test_captured_step_grows_the_cache():
                           tk[:, (4 + Hk) * D:].reshape(B, Hk, D).numpy(), slots, page)
             want, bound = ref.attention(x[:, : 4 * D].reshape(B, 4, D), cache, table, [i + 1] * B, [0, 1, 2, 3], page, D ** -0.5)
             assert bool(((out.cpu().double() - want).abs() <= bound).all())
+
+
+def test_mixed_batches():
+    # prompts, chunks and single tokens in one call: two kernels share the requests between them
+    lens = [700, 33, 512, 1, 2000, 90, 0, 300, 64]
+    new = [500, 1, 12, 1, 60, 90, 0, 13, 3]
+    for D, Hk, group, page in ((128, 2, 4, 16), (64, 1, 7, 32)):
+        p, c, table = _filled(lens, Hk, D, page, seed=D)
+        cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+        q = _rows(cu[-1] + 5, Hk * group, D, 17)
+        _check_attention(c, table, q, cu, lens, max(new))
+        _check_attention(c, table, q, cu, lens, max(new), window=100)
+    # many requests of which a few have queries
+    lens = [20 + i % 50 for i in range(600)]
+    new = [0] * 600
+    for i in range(0, 600, 37):
+        new[i] = 1 + i % 19
+    new[599], lens[599] = 60, 69
+    p, c, table = _filled(lens, 1, 64, 16, seed=77)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    _check_attention(c, table, _rows(cu[-1], 4, 64, 3), cu, lens, 60)
+
+
+@pytest.mark.parametrize("new", [1, 6, 40])
+def test_pages_before_the_window_may_be_gone(new):
+    # a sliding window's user frees the pages that no query sees any more
+    for page, window, n in ((16, 50, 500), (32, 64, 333), (128, 200, 1000)):
+        p, c, table = _filled([n, 3 * page], 2, 64, page, seed=page)
+        first = n - new - window + 1           # the first position that a query of request 0 sees
+        gone = first // page
+        assert gone > 0
+        p.block_table[0, :gone] = -1
+        q = _rows(2 * new, 8, 64, 5)
+        _check_attention(c, table, q, [0, new, 2 * new], [n, 3 * page], new, window=window)

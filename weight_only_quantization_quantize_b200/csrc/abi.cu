@@ -607,13 +607,6 @@ awq::Kv4Cache kv4_cache(const uint8_t *data, int64_t kv_heads, int64_t D, int64_
                          page_shift_of(page_size)};
 }
 
-// Query rows per key/value head and request from which the prompt kernel takes
-// over.  The split kernel covers 16 rows per pass over the cache, the prompt
-// kernel 256, at a higher fixed cost.  Measured, split against prompt kernel, in
-// us: 32 rows 39 / 47 (1 x 32000 keys), 47 / 77 (16 x 4000); 64 rows 57 / 49 and
-// 156 / 100 (32 x 4000); 128 rows 94 / 51.
-constexpr int64_t kPrefillRows = 48;
-
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 }  // namespace
 
@@ -744,9 +737,13 @@ awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, i
     a.window = static_cast<int>(window);
     a.scale = scale;
     a.status = dev_status;
-    if (max_new * (q_heads / kv_heads) > kPrefillRows)
-        return from_cuda(awq::launch_kv4_prefill(a, workspace, sms, static_cast<cudaStream_t>(stream)));
-    return from_cuda(awq::launch_kv4_attend(a, workspace, sms, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (max_new * (q_heads / kv_heads) <= awq::kPromptRows)
+        return from_cuda(awq::launch_kv4_attend(a, INT64_MAX, workspace, sms, st));
+    // the requests with many rows, then those with few
+    e = from_cuda(awq::launch_kv4_prefill(a, workspace, sms, st));
+    if (e == AWQ_OK) e = from_cuda(awq::launch_kv4_attend(a, awq::kPromptRows, workspace, sms, st));
+    return e;
 }
 
 }  // extern "C"

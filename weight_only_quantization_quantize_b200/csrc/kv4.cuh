@@ -64,11 +64,18 @@ struct Kv4AttendArgs {
     float scale;
     int32_t *status;
 };
+// Query rows (queries times heads of a group) of a request above which the prompt
+// kernel takes it.  The split kernel covers 16 rows per pass over the cache, the
+// prompt kernel 256, at a higher fixed cost.  Measured, split against prompt
+// kernel, in us: 32 rows 39 / 47 (1 x 32000 keys), 47 / 77 (16 x 4000); 64 rows
+// 57 / 49 and 156 / 100 (32 x 4000); 128 rows 94 / 51.
+constexpr int kPromptRows = 48;
 cudaError_t configure_kv4_attend();
 size_t kv4_attend_workspace(int D);
-cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, void *ws, int num_sms, cudaStream_t st);
+// requests with more than max_rows rows are left to the prompt kernel
+cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, int64_t max_rows, void *ws, int num_sms, cudaStream_t st);
 
-// kv4_prefill.cu -- many query rows per key/value head: tcgen05
+// kv4_prefill.cu -- the requests with more than kPromptRows rows: tcgen05
 cudaError_t configure_kv4_prefill();
 size_t kv4_prefill_workspace(int D);
 cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, void *ws, int num_sms, cudaStream_t st);

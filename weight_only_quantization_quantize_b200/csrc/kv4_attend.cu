@@ -32,6 +32,8 @@
 // A CTA is four independent warps with a ring of kStages tiles each, filled by
 // bulk copies that the warp's lanes issue in turn: a block of 16 tokens (keys,
 // values, steps, zero points) is one contiguous piece of the page.
+#include <type_traits>
+
 #include "awq_kernels.cuh"
 #include "kv4.cuh"
 
@@ -80,11 +82,13 @@ struct Params {
     float2 *ml;      // [2 grid][rows]: (reference, sum) of a part
     float *part;     // [2 grid][rows][D]
     int group;
+    int64_t max_rows;  // requests with more rows are another kernel's
     UnpackConsts uk;
 };
 
 struct Request {
     int len, nq, q0;   // cached tokens, queries, first query row
+    int lo;            // the first position that any query sees
     int tile0, tiles;  // first tile that any query reads, tiles from there
     int items;         // row blocks times heads
     int units;         // of one item: its tiles, and kItemCost for what it costs besides
@@ -112,10 +116,11 @@ __device__ __forceinline__ Request request_at(const Params &p, int b)
     if (bad) report(a.status, AWQ_ERR_RANGE);
     r.nq = static_cast<int>(nq);
     const long long first = a.window > 0 ? static_cast<long long>(r.len) - r.nq - a.window + 1 : 0;
-    r.tile0 = first > 0 ? static_cast<int>(first) / kTile : 0;
+    r.lo = first > 0 ? static_cast<int>(first) : 0;
+    r.tile0 = r.lo / kTile;
     const int t = (r.len + kTile - 1) / kTile - r.tile0;
     r.tiles = t < 1 ? 1 : t;  // rows that see nothing are still written
-    r.items = (r.nq * p.group + ROWS - 1) / ROWS * a.cache.heads;
+    r.items = static_cast<int64_t>(r.nq) * p.group > p.max_rows ? 0 : (r.nq * p.group + ROWS - 1) / ROWS * a.cache.heads;
     r.units = r.tiles + kItemCost;
     return r;
 }
@@ -268,9 +273,10 @@ __device__ __forceinline__ void start_item(Warp<D, NT> &w, const Params &p, cons
 
 // Two blocks, 32 tokens tok .. tok + 31.  full: every token is seen by every
 // row, and every row has a reference; otherwise rows are masked and blocks
-// whose bit in `have` is clear hold nothing.
-template <int D, int NT>
-__device__ __forceinline__ void tile_step(Warp<D, NT> &w, const uint8_t *stage, int tok, bool full, int have, float c1,
+// whose bit in `have` is clear hold nothing.  NT of the warp's WT column tiles
+// hold rows.
+template <int D, int WT, int NT>
+__device__ __forceinline__ void tile_step(Warp<D, WT> &w, const uint8_t *stage, int tok, bool full, int have, float c1,
                                           const UnpackConsts &uk, int lane)
 {
     constexpr int KW = D / 32;  // key words per lane and row
@@ -573,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
             const int tok = (lr.tile0 + lt0 + tl) * kTile + kKvBlock * j;
             const int sh = a.cache.page_shift - 4;
             bool there = false;
-            if (tl < lseg && tok < lr.len) {
+            // blocks before the first position that any query sees may have lost their pages
+            if (tl < lseg && tok < lr.len && tok + kKvBlock > lr.lo) {
                 const int page = a.tab.block_table[static_cast<size_t>(lb) * a.tab.max_pages + (tok >> a.cache.page_shift)];
                 there = page >= 0 && page < a.cache.num_pages;
                 if (!there) report(a.status, AWQ_ERR_RANGE);
@@ -582,9 +589,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
             }
             held = (__ballot_sync(0xffffffffu, there) >> (lane & 28)) & 15;
             expect = __popc(held) * C::kBlock;
-            // blocks of one page lie together: its first block's lane copies them all
-            const int run = sh > 2 ? 4 : 1 << sh;
-            bytes = there && j % run == 0 ? __popc((held >> j) & ((1 << run) - 1)) * C::kBlock : 0;
+            // the blocks of one page that are there lie together: the first one's lane copies them all
+            const int size = sh > 2 ? 4 : 1 << sh, begin = j & ~(size - 1);
+            const bool lead = there && (j == begin || !((held >> (j - 1)) & 1));
+            bytes = lead ? __popc((held >> j) & ((1 << (begin + size - j)) - 1)) * C::kBlock : 0;
         }
         if ((lane >> 2) == turn) {
             const uint32_t mb = bar0 + 8 * ist;
@@ -622,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
         if (warp < seg) {
             start_item<D, NT>(w, p, r, item, lane);
             const int rb = item / heads;
+            const bool wide = r.nq * p.group - rb * C::kRows > 8;
             const int ifirst = rb * C::kRows / p.group;
             const int ilast = min((rb * C::kRows + C::kRows - 1) / p.group, r.nq - 1);
             const int pfirst = r.len - r.nq + ifirst;                       // the earliest row's position
@@ -638,15 +647,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
                 }
                 const uint8_t *stage = smem + warp * (C::kStages * C::kStage) + st * C::kStage;
                 const int have = have_of[st];
-                if (ready && have == (1 << kTileBlocks) - 1 && k >= first && k < last) {
+                // the second column tile may hold no rows (single tokens among longer runs)
+                auto blocks = [&](auto tiles, bool full) {
+                    constexpr int A = decltype(tiles)::value;
+                    if (full) {
 #pragma unroll
-                    for (int b = 0; b < kTileBlocks; b += 2)
-                        tile_step<D, NT>(w, stage + b * C::kBlock, 0, true, 3, c1, p.uk, lane);
-                } else {
-                    for (int b = 0; b < kTileBlocks; b += 2)
-                        if ((have >> b) & 3)
-                            tile_step<D, NT>(w, stage + b * C::kBlock, (base + k) * kTile + b * kKvBlock, false,
-                                             (have >> b) & 3, c1, p.uk, lane);
+                        for (int b = 0; b < kTileBlocks; b += 2)
+                            tile_step<D, NT, A>(w, stage + b * C::kBlock, 0, true, 3, c1, p.uk, lane);
+                    } else {
+                        for (int b = 0; b < kTileBlocks; b += 2)
+                            if ((have >> b) & 3)
+                                tile_step<D, NT, A>(w, stage + b * C::kBlock, (base + k) * kTile + b * kKvBlock, false,
+                                                    (have >> b) & 3, c1, p.uk, lane);
+                    }
+                };
+                const bool full = ready && have == (1 << kTileBlocks) - 1 && k >= first && k < last;
+                if (NT == 1 || wide)
+                    blocks(std::integral_constant<int, NT>{}, full);
+                else
+                    blocks(std::integral_constant<int, 1>{}, full);
+                if (!full) {
                     bool set = true;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) set = set && w.m[n][0] != -INFINITY && w.m[n][1] != -INFINITY;
@@ -884,7 +904,7 @@ size_t kv4_attend_workspace(int D)
     return kDescBytes + kMlBytes + sizeof(float) * 2 * kMaxCtas * kMaxRows * static_cast<size_t>(D);
 }
 
-cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, void *ws, int num_sms, cudaStream_t st)
+cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, int64_t max_rows, void *ws, int num_sms, cudaStream_t st)
 {
     uint8_t *w = static_cast<uint8_t *>(ws);
     Params prm{};
@@ -893,9 +913,11 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, void *ws, int num_sms, cud
     prm.ml = reinterpret_cast<float2 *>(w + kDescBytes);
     prm.part = reinterpret_cast<float *>(w + kDescBytes + kMlBytes);
     prm.group = a.q_heads / a.cache.heads;
+    prm.max_rows = max_rows;
     prm.uk = unpack_consts();
     // 8 query rows per key/value head fill one MMA column tile, more take two
-    const bool narrow = static_cast<int64_t>(a.max_new) * prm.group <= 8;
+    const int64_t rows = static_cast<int64_t>(a.max_new) * prm.group;
+    const bool narrow = (rows < max_rows ? rows : max_rows) <= 8;
     if (a.cache.D == 128)
         return narrow ? launch_one<128, 1>(prm, num_sms, st) : launch_one<128, 2>(prm, num_sms, st);
     return narrow ? launch_one<64, 1>(prm, num_sms, st) : launch_one<64, 2>(prm, num_sms, st);

@@ -32,6 +32,7 @@
 // one could have left binary16; only then (or while a row has no reference yet, or
 // under a mask) a warp looks for the maximum, moves the reference, rescales its
 // output rows and computes the weights again.
+#include <algorithm>
 #include <type_traits>
 
 #include "awq_kernels.cuh"
@@ -69,13 +70,18 @@ struct Cfg {
     static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * kTile + kStepBytes + 256;
 };
 
+// What the joining kernel has to know of a row block.
+struct BlockRows {
+    int q0, first, rows, pad;  // the request's first query row; the block's first row; the request's rows
+};
+
 struct Params {
     Kv4AttendArgs a;
     int group;
-    int blocks;    // row blocks of a request and head at most
-    int splits;    // parts of every row block's keys, one CTA each
-    float2 *ml;    // splits > 1, [row block][split][256]: (reference, sum) of a row
-    float *part;   // [row block][split][256][D]: its numerators
+    int splits;      // parts of every row block's keys, one CTA each
+    BlockRows *rows; // splits > 1, [row block]
+    float2 *ml;      // [row block][head][split][256]: (reference, sum) of a row
+    float *part;     // [row block][head][split][256][D]: its numerators
     UnpackConsts uk;
 };
 
@@ -217,25 +223,65 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // ---------------------------------------------------------------- this CTA's rows and keys
-    // later row blocks see more keys: they come first
-    const int b = static_cast<int>(blockIdx.z), head = static_cast<int>(blockIdx.y);
-    const int rb = p.blocks - 1 - static_cast<int>(blockIdx.x) / p.splits;
-    const int split = static_cast<int>(blockIdx.x) % p.splits;
+    // Row blocks of 256 rows, request after request, and in each the last one
+    // first (it sees the most keys).  blockIdx.x counts them for the requests
+    // that are this kernel's, found by a scan over all requests.
+    const int head = static_cast<int>(blockIdx.y);
+    const int flat = static_cast<int>(blockIdx.x) / p.splits, split = static_cast<int>(blockIdx.x) % p.splits;
+    __shared__ int s_warp[kThreads / 32], s_request, s_block;
+    auto rows_of = [&](int b) -> int {  // of request b, 0 when it is not this kernel's
+        const int q0 = a.tab.cu ? a.tab.cu[b] : b;
+        const long long q1 = a.tab.cu ? a.tab.cu[b + 1] : b + 1, n = q1 - q0;
+        if (q0 < 0 || n < 0 || q1 > a.T || n > a.max_new) {
+            if (blockIdx.x == 0 && head == 0) report(a.status, AWQ_ERR_RANGE);
+            return 0;
+        }
+        const long long rows = n * p.group;
+        return rows > kPromptRows ? static_cast<int>(rows) : 0;
+    };
+    {
+        if (threadIdx.x == 0) s_request = -1;
+        const int per = (a.tab.B + kThreads - 1) / kThreads, b0 = static_cast<int>(threadIdx.x) * per;
+        int mine = 0;
+        for (int i = 0; i < per && b0 + i < a.tab.B; ++i) mine += (rows_of(b0 + i) + kRowsCta - 1) / kRowsCta;
+        int pre = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, pre, d);
+            if (lane >= d) pre += y;
+        }
+        if (lane == 31) s_warp[warp] = pre;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) pre += s_warp[i];
+        pre -= mine;
+        if (flat >= pre && flat < pre + mine) {
+            int rem = flat - pre, b = b0, n = (rows_of(b) + kRowsCta - 1) / kRowsCta;
+            while (rem >= n && b + 1 < a.tab.B) {
+                rem -= n;
+                n = (rows_of(++b) + kRowsCta - 1) / kRowsCta;
+            }
+            s_request = b;
+            s_block = n - 1 - rem;
+        }
+        __syncthreads();
+    }
+    const int b = s_request;
+    if (b < 0) {
+        if (p.splits > 1 && head == 0 && split == 0 && threadIdx.x == 0) p.rows[flat].rows = 0;
+        return;
+    }
+    const int rb = s_block;
     const long long most = static_cast<long long>(a.tab.max_pages) << a.cache.page_shift;
     int len = a.tab.lens[b];
     const int q0 = a.tab.cu ? a.tab.cu[b] : b;
-    const long long q1 = a.tab.cu ? a.tab.cu[b + 1] : b + 1;
-    const long long nql = q1 - q0;
-    const bool bad_rows = q0 < 0 || nql < 0 || q1 > a.T || nql > a.max_new;
-    if (threadIdx.x == 0 && rb == 0 && head == 0 && split == 0 && (bad_rows || len < 0 || len > most)) report(a.status, AWQ_ERR_RANGE);
-    const int nq = bad_rows ? 0 : static_cast<int>(nql);
+    const int rows = rows_of(b), nq = rows / p.group;
+    if (threadIdx.x == 0 && head == 0 && split == 0 && (len < 0 || len > most)) report(a.status, AWQ_ERR_RANGE);
     len = len < 0 ? 0 : len > most ? static_cast<int>(most) : len;
-    const long long rows = static_cast<long long>(nq) * p.group;
-    const long long row0 = static_cast<long long>(rb) * kRowsCta;
-    if (row0 >= rows) return;
+    const int row0 = rb * kRowsCta;
+    if (p.splits > 1 && head == 0 && split == 0 && threadIdx.x == 0) p.rows[flat] = BlockRows{q0, row0, rows, 0};
     const int ntiles_q = row0 + kRowsTile < rows ? 2 : 1;
-    const int rlast = static_cast<int>((row0 + kRowsCta < rows ? row0 + kRowsCta : rows) - 1);
-    const int pfirst = max(len - nq + static_cast<int>(row0 / p.group), -1);  // positions; -1: before the first token
+    const int rlast = min(row0 + kRowsCta, rows) - 1;
+    const int pfirst = max(len - nq + row0 / p.group, -1);  // positions; -1: before the first token
     const int plast = max(len - nq + rlast / p.group, -1);
     const int lo_first = a.window > 0 ? max(pfirst - a.window + 1, 0) : 0;
     // this split's share of the key tiles
@@ -283,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
             const uint32_t ts = tmem + lanes + t * kKeys;
             const uint32_t to = tmem + lanes + C::kOCol + t * D;
             const int r = 32 * (warp & 3) + lane;  // row of the tile
-            const long long row = row0 + t * kRowsTile + r;
+            const int row = row0 + t * kRowsTile + r;
             const bool in = row < rows;
-            const int qi = in ? static_cast<int>(row / p.group) : 0;
-            const int qh = head * p.group + (in ? static_cast<int>(row - static_cast<long long>(qi) * p.group) : 0);
+            const int qi = in ? row / p.group : 0;
+            const int qh = head * p.group + (in ? row - qi * p.group : 0);
             // The warp's 32 query rows into the swizzled tile, W lanes per row,
             // channels of each 8 in the order (0,4),(1,5),(2,6),(3,7) that the
             // unpack gives the keys.
@@ -296,11 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     const int rr = 32 * (warp & 3) + i * (32 / W) + lane / W;
-                    const long long rw = row0 + t * kRowsTile + rr;
+                    const int rw = row0 + t * kRowsTile + rr;
                     x[i] = make_uint4(0, 0, 0, 0);
                     if (rw < rows) {
-                        const int ri = static_cast<int>(rw) / p.group;
-                        const int rh = head * p.group + static_cast<int>(rw) - ri * p.group;
+                        const int ri = rw / p.group;
+                        const int rh = head * p.group + rw - ri * p.group;
                         x[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + (q0 + ri) * a.q_stride + static_cast<int64_t>(rh) * D) + c);
                     }
                 }
@@ -320,10 +366,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
             const int lo = a.window > 0 ? pos - a.window : -1;
             // positions of the tile's first and last row: a key tile that every
             // row sees needs no mask
-            const long long rt = row0 + t * kRowsTile;
-            const long long re = rt + kRowsTile - 1 < rows - 1 ? rt + kRowsTile - 1 : rows - 1;
-            const int p_lo = max(len - nq + static_cast<int>(rt / p.group), -1);
-            const int w_hi = a.window > 0 ? max(len - nq + static_cast<int>(re / p.group), -1) - a.window : -1;
+            const int rt = row0 + t * kRowsTile, re = min(rt + kRowsTile, rows) - 1;
+            const int p_lo = max(len - nq + rt / p.group, -1);
+            const int w_hi = a.window > 0 ? max(len - nq + re / p.group, -1) - a.window : -1;
             float m = in ? -INFINITY : 0.0f, l = 0.0f;
             bool ok = true, ready = false;
             for (int j = 0; j < tiles; ++j) {
@@ -504,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 tc_fence_after();
                 if (p.splits > 1) {
                     // numerators, reference and sum for the join
-                    const size_t at = ((static_cast<size_t>(b) * gridDim.y + head) * p.blocks + rb) * p.splits + split;
+                    const size_t at = (static_cast<size_t>(flat) * gridDim.y + head) * p.splits + split;
                     const size_t slot = at * kRowsCta + t * kRowsTile + r;
                     if (in) p.ml[slot] = make_float2(m, l);
 #pragma unroll 1
@@ -558,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
         // codes and steps of tile j's token; false where there is none
         auto fetch = [&](int j, uint4 (&kx)[W / 4], uint4 (&vx)[W / 4], uint32_t &km, uint32_t &vm) -> bool {
             const int tok = (tile0 + j) * kKeys + tok_in;
-            bool there = j < tiles && tok < end;
+            bool there = j < tiles && tok < end && tok >= lo_first;  // pages before the window may be gone
             if (there) {
                 const int page = table[tok >> a.cache.page_shift];
                 if (page < 0 || page >= a.cache.num_pages) {
@@ -731,15 +776,12 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p)
     constexpr int E = D / 32;
     pdl_wait();
     const Kv4AttendArgs &a = p.a;
-    const int b = static_cast<int>(blockIdx.z), head = static_cast<int>(blockIdx.y);
-    const int rb = static_cast<int>(blockIdx.x) / (kRowsCta / 8);
+    const int flat = static_cast<int>(blockIdx.x) / (kRowsCta / 8), head = static_cast<int>(blockIdx.y);
     const int r = static_cast<int>(blockIdx.x) % (kRowsCta / 8) * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int q0 = a.tab.cu ? a.tab.cu[b] : b;
-    const long long q1 = a.tab.cu ? a.tab.cu[b + 1] : b + 1, nq = q1 - q0;
-    if (q0 < 0 || nq < 0 || q1 > a.T || nq > a.max_new) return;
-    const long long row = static_cast<long long>(rb) * kRowsCta + r;
-    if (row >= nq * p.group) return;
-    const size_t first = ((static_cast<size_t>(b) * gridDim.y + head) * p.blocks + rb) * p.splits;
+    const BlockRows br = p.rows[flat];
+    const int row = br.first + r;
+    if (row >= br.rows) return;
+    const size_t first = (static_cast<size_t>(flat) * gridDim.y + head) * p.splits;
     auto slot = [&](int s) { return (first + s) * kRowsCta + r; };
     float top = -INFINITY;
     for (int s = lane; s < p.splits; s += 32) top = fmaxf(top, p.ml[slot(s)].x);
@@ -758,20 +800,24 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p)
         for (int e = 0; e < E; ++e) o[e] += p.part[slot(s) * D + E * lane + e] * f;
     }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int qi = static_cast<int>(row) / p.group;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (static_cast<int64_t>(q0 + qi) * a.q_heads + head * p.group +
-                                                           static_cast<int>(row) - qi * p.group) * D + E * lane);
+    const int qi = row / p.group;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + (static_cast<int64_t>(br.q0 + qi) * a.q_heads + head * p.group +
+                                                           row - qi * p.group) * D + E * lane);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = pack2(o[e] * inv, o[e + 1] * inv);
 }
 
 // Partial results that the workspace holds, 256 rows each.
 constexpr int kMaxParts = 160;
+constexpr size_t kBlockBytes = (sizeof(BlockRows) * kMaxParts + 255) / 256 * 256;
 constexpr size_t kMlBytes = sizeof(float2) * kMaxParts * kRowsCta;
 
 }  // namespace
 
-size_t kv4_prefill_workspace(int D) { return kMlBytes + sizeof(float) * kMaxParts * kRowsCta * static_cast<size_t>(D); }
+size_t kv4_prefill_workspace(int D)
+{
+    return kBlockBytes + kMlBytes + sizeof(float) * kMaxParts * kRowsCta * static_cast<size_t>(D);
+}
 
 cudaError_t configure_kv4_prefill()
 {
@@ -788,21 +834,26 @@ cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, void *ws, int num_sms, cu
     prm.a = a;
     prm.group = a.q_heads / a.cache.heads;
     prm.uk = unpack_consts();
-    const int64_t new_rows = (a.max_new < a.T ? a.max_new : a.T) * static_cast<int64_t>(prm.group);
-    prm.blocks = static_cast<int>((new_rows + kRowsCta - 1) / kRowsCta);
+    // Row blocks at most: T queries in whole blocks, and one cut block for each
+    // request that has enough rows to be this kernel's.
+    const int64_t all = a.T * prm.group, of_one = (std::min<int64_t>(a.max_new, a.T) * prm.group + kRowsCta - 1) / kRowsCta;
+    const int64_t requests = std::min<int64_t>(a.tab.B, all / (kPromptRows + 1));
+    const int64_t bound = std::min(all / kRowsCta + requests, of_one * a.tab.B);
+    if (bound == 0) return cudaSuccess;  // too few queries for any such request
     // Few row blocks leave SMs idle: their keys are split until the GPU is full,
     // into parts of at least four tiles (by the table's width, the only length
     // known here).
-    const int64_t blocks = static_cast<int64_t>(prm.blocks) * a.cache.heads * a.tab.B;
+    const int64_t blocks = bound * a.cache.heads;
     const int sms = num_sms < kMaxParts ? num_sms : kMaxParts;
     const int64_t by_keys = (static_cast<int64_t>(a.tab.max_pages) << a.cache.page_shift) / (4 * kKeys);
     int64_t splits = blocks < sms ? sms / blocks : 1;
     if (splits > by_keys) splits = by_keys < 1 ? 1 : by_keys;
     prm.splits = static_cast<int>(splits);
-    prm.ml = static_cast<float2 *>(ws);
-    prm.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kMlBytes);
-    const dim3 grid(static_cast<unsigned>(prm.blocks * prm.splits), static_cast<unsigned>(a.cache.heads),
-                    static_cast<unsigned>(a.tab.B));
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    prm.rows = reinterpret_cast<BlockRows *>(w);
+    prm.ml = reinterpret_cast<float2 *>(w + kBlockBytes);
+    prm.part = reinterpret_cast<float *>(w + kBlockBytes + kMlBytes);
+    const dim3 grid(static_cast<unsigned>(bound * splits), static_cast<unsigned>(a.cache.heads));
     if (a.cache.D == 128)
         prefill_kernel<128><<<grid, kThreads, Cfg<128>::kSmem, st>>>(prm);
     else
@@ -810,7 +861,7 @@ cudaError_t launch_kv4_prefill(const Kv4AttendArgs &a, void *ws, int num_sms, cu
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || prm.splits == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(prm.blocks) * (kRowsCta / 8), grid.y, grid.z);
+    cfg.gridDim = dim3(static_cast<unsigned>(bound) * (kRowsCta / 8), grid.y, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
