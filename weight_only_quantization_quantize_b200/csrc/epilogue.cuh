@@ -12,6 +12,8 @@
 // their own bytes (2 N + 2 M N) and no further pass over Y.
 #pragma once
 
+#include <type_traits>
+
 #include "awq_common.cuh"
 
 namespace awq {
@@ -30,17 +32,37 @@ __device__ __forceinline__ float epi_sigmoid_times(float t, float u)  // t * sig
     return __fdividef(t, 1.0f + __expf(-u));
 }
 
-__device__ __forceinline__ float epi_act(float t, int act)
+template <int ACT>
+__device__ __forceinline__ float epi_act_of(float t)
+{
+    if constexpr (ACT == AWQ_ACT_RELU) return t < 0.0f ? 0.0f : t;  // NaN stays NaN
+    if constexpr (ACT == AWQ_ACT_SILU) return epi_sigmoid_times(t, t);
+    if constexpr (ACT == AWQ_ACT_GELU) return 0.5f * t * erfcf(-0.70710678f * t);
+    // 0.5 t (1 + tanh(u)) = t sigmoid(2u), u = sqrt(2/pi) (t + 0.044715 t^3)
+    if constexpr (ACT == AWQ_ACT_GELU_TANH) return epi_sigmoid_times(t, 1.59576912f * (t + 0.044715f * t * t * t));
+    return t;
+}
+
+// f(integral_constant<int, act>): the choice is made once per call, not per
+// value.  (Inside unrolled loops it multiplied the code by the five activations:
+// the prompt kernels then ran out of the instruction cache, and a bias alone
+// took 2048 x 4096 x 28672 from 424 to 526 us, a gate to 691.)
+template <class F>
+__device__ __forceinline__ void epi_with_act(int act, F &&f)
 {
     switch (act) {
-    case AWQ_ACT_RELU: return t < 0.0f ? 0.0f : t;  // NaN stays NaN
-    case AWQ_ACT_SILU: return epi_sigmoid_times(t, t);
-    case AWQ_ACT_GELU: return 0.5f * t * erfcf(-0.70710678f * t);
-    case AWQ_ACT_GELU_TANH:
-        // 0.5 t (1 + tanh(u)) = t sigmoid(2u), u = sqrt(2/pi) (t + 0.044715 t^3)
-        return epi_sigmoid_times(t, 1.59576912f * (t + 0.044715f * t * t * t));
-    default: return t;
+    case AWQ_ACT_RELU: f(std::integral_constant<int, AWQ_ACT_RELU>{}); break;
+    case AWQ_ACT_SILU: f(std::integral_constant<int, AWQ_ACT_SILU>{}); break;
+    case AWQ_ACT_GELU: f(std::integral_constant<int, AWQ_ACT_GELU>{}); break;
+    case AWQ_ACT_GELU_TANH: f(std::integral_constant<int, AWQ_ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, AWQ_ACT_NONE>{}); break;
     }
+}
+
+__device__ __forceinline__ float epi_act(float t, int act)
+{
+    epi_with_act(act, [&](auto a) { t = epi_act_of<decltype(a)::value>(t); });
+    return t;
 }
 
 __device__ __forceinline__ float epi_bias(const Epilogue &e, int n)
@@ -70,8 +92,10 @@ __device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __h
         }
     }
     if (e.gated) {
+        epi_with_act(e.act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = epi_act(v[2 * i], e.act) * v[2 * i + 1];
+            for (int i = 0; i < 4; ++i) v[i] = epi_act_of<decltype(a)::value>(v[2 * i]) * v[2 * i + 1];
+        });
         const size_t at = static_cast<size_t>(tok) * (N / 2) + n / 2;
         if (e.residual) {
             const uint2 r = *reinterpret_cast<const uint2 *>(e.residual + at);
@@ -80,8 +104,10 @@ __device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __h
         *reinterpret_cast<uint2 *>(Y + at) = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
         return;
     }
+    epi_with_act(e.act, [&](auto a) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = epi_act(v[i], e.act);
+        for (int i = 0; i < 8; ++i) v[i] = epi_act_of<decltype(a)::value>(v[i]);
+    });
     const size_t at = static_cast<size_t>(tok) * N + n;
     if (e.residual) {
         const uint4 r = *reinterpret_cast<const uint4 *>(e.residual + at);
@@ -114,11 +140,13 @@ __device__ __forceinline__ void epi_store_column32(const Epilogue &e, float (&v)
         const bool odd = n & 1;
         const int cols = N / 2;
         float o[16];
+        epi_with_act(e.act, [&](auto a) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float x = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
-            o[i] = odd ? epi_act(x, e.act) * v[2 * i + 1] : epi_act(v[2 * i], e.act) * x;
-        }
+            for (int i = 0; i < 16; ++i) {
+                const float x = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+                o[i] = epi_act_of<decltype(a)::value>(odd ? x : v[2 * i]) * (odd ? v[2 * i + 1] : x);
+            }
+        });
         if (!in) return;
         const int first = odd ? 1 : 0;
         const size_t at = static_cast<size_t>(m0 + first) * cols + n / 2;
@@ -139,8 +167,10 @@ __device__ __forceinline__ void epi_store_column32(const Epilogue &e, float (&v)
         return;
     }
     if (!in) return;
+    epi_with_act(e.act, [&](auto a) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = epi_act(v[i], e.act);
+        for (int i = 0; i < 32; ++i) v[i] = epi_act_of<decltype(a)::value>(v[i]);
+    });
     const size_t at = static_cast<size_t>(m0) * N + n;
     if (e.residual) {
         const __half *r = e.residual + at;
