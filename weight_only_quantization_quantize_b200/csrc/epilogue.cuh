@@ -122,6 +122,18 @@ __device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __h
                                                     pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
 }
 
+// The residual of token `tok`, columns n0 .. n0 + 127 before the gate, on its way
+// into L2 while the products run: the epilogue then waits for L2, not for HBM.
+__device__ __forceinline__ void epi_prefetch_row128(const Epilogue &e, int tok, int M, int n0, int N)
+{
+    if (e.residual == nullptr || tok >= M) return;
+    const int cols = e.gated ? N / 2 : N, c0 = e.gated ? n0 / 2 : n0;
+    const int c1 = min(c0 + (e.gated ? 64 : 128), cols);
+    const __half *row = e.residual + static_cast<size_t>(tok) * cols;
+    for (int c = c0; c < c1; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c1 - 1));
+}
+
 // 32 tokens m0 .. m0 + 31 (those below m0 + mrem) of column n, one column per
 // lane (the accumulator layout of the tcgen05 kernels, n = n0 + lane with n0
 // even); every lane of the warp calls it, lanes with n >= N write nothing.

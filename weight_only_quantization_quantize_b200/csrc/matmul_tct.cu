@@ -210,6 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = (warp - 2) >> 2;
         const int col = quarter * 32 + lane;  // column within the tile
         const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+        if constexpr (EPI)
+            for (int i = threadIdx.x - 64; i < BT; i += 32 * kDequantWarps) epi_prefetch_row128(p.epi, m0 + i, p.M, n0, p.N);
         const UnpackConsts uk = p.uk;
         bool ok = true;
         for (int kb = 0; kb < KB; ++kb) {

@@ -330,6 +330,10 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
         int seg = 0;
         for (int64_t u = u_begin; u < u_end && ok; ++seg) {
             const Segment sg = segment_at(u, u_end, S);
+            if constexpr (EPI)
+                if (sg.s0 == 0)  // this CTA will write the tile
+                    for (int i = threadIdx.x - 64; i < BT; i += 32 * kDequantWarps)
+                        epi_prefetch_row128(p.epi, (sg.tile % p.m_tiles) * BT + i, p.M, (sg.tile / p.m_tiles) * kCols, p.N);
             for (int kb = sg.s0; kb < sg.s1; ++kb) {
                 bool w = mbar_wait(&full_load[st], ph);
                 if (w && it >= kASlots) w = mbar_wait(&empty_a[as], pa ^ 1u);
