@@ -134,15 +134,35 @@ __device__ __forceinline__ void epi_prefetch_row128(const Epilogue &e, int tok, 
     asm volatile("prefetch.global.L2 [%0];" ::"l"(row + c1 - 1));
 }
 
+// The residual of 32 tokens and column n as epi_store_column32 wants it: before
+// the sums are complete, so that its latency is not added to theirs.
+__device__ __forceinline__ void epi_load_column32(const Epilogue &e, uint32_t (&rv)[16], int m0, int mrem, int n, int N)
+{
+    const int first = n & 1;
+    if (e.residual == nullptr || n >= N) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) rv[i] = 0u;
+    } else if (e.gated) {
+        const int cols = N / 2;
+        const uint16_t *r = reinterpret_cast<const uint16_t *>(e.residual) + static_cast<size_t>(m0 + first) * cols + n / 2;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) rv[i] = 2 * i + first < mrem ? r[2 * static_cast<size_t>(i) * cols] : 0u;
+    } else {
+        const uint32_t *r = reinterpret_cast<const uint32_t *>(e.residual) + (static_cast<size_t>(m0 + first) * N + (n & ~1)) / 2;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) rv[i] = 2 * i + first < mrem ? r[static_cast<size_t>(i) * N] : 0u;
+    }
+}
+
 // 32 tokens m0 .. m0 + 31 (those below m0 + mrem) of column n, one column per
 // lane (the accumulator layout of the tcgen05 kernels, n = n0 + lane with n0
 // even); every lane of the warp calls it, lanes with n >= N write nothing.
 // Gated: lanes 2j and 2j + 1 hold a gate and its column; the even lane
 // finishes the even tokens and the odd lane the odd ones, one exchange per
-// token pair.  The residual is read before the first store: Y may be the
-// residual's own memory.
-__device__ __forceinline__ void epi_store_column32(const Epilogue &e, float (&v)[32], __half *Y, int m0, int mrem,
-                                                   int n, int N)
+// token pair.  rv: the residual, from epi_load_column32 (all of it was read
+// before the first store: Y may be the residual's own memory).
+__device__ __forceinline__ void epi_store_column32(const Epilogue &e, float (&v)[32], const uint32_t (&rv)[16],
+                                                   __half *Y, int m0, int mrem, int n, int N)
 {
     const bool in = n < N;
     const float b = in ? epi_bias(e, n) : 0.0f;
@@ -163,40 +183,41 @@ __device__ __forceinline__ void epi_store_column32(const Epilogue &e, float (&v)
         const int first = odd ? 1 : 0;
         const size_t at = static_cast<size_t>(m0 + first) * cols + n / 2;
         const size_t step = 2 * static_cast<size_t>(cols);
-        if (e.residual) {
-            const __half *r = e.residual + at;
-            __half rv[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                rv[i] = 2 * i + first < mrem ? r[i * step] : __half(__ushort_as_half(0));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] += __half2float(rv[i]);
-        }
+        for (int i = 0; i < 16; ++i) o[i] += half_lo(rv[i]);
         __half *dst = Y + at;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             if (2 * i + first < mrem) dst[i * step] = __float2half_rn(o[i]);
         return;
     }
-    if (!in) return;
     epi_with_act(e.act, [&](auto a) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = epi_act_of<decltype(a)::value>(v[i]);
     });
-    const size_t at = static_cast<size_t>(m0) * N + n;
-    if (e.residual) {
-        const __half *r = e.residual + at;
-        __half rv[32];
+    // the even lane of a pair finishes both its columns of the even tokens, the odd
+    // lane of the odd ones: 4-byte accesses, half as many (N is even)
+    const bool odd = n & 1;
+    float o[32];  // of token 2 i + odd: columns n & ~1 and the next
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            rv[i] = i < mrem ? r[static_cast<size_t>(i) * N] : __half(__ushort_as_half(0));
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __half2float(rv[i]);
+    for (int i = 0; i < 16; ++i) {
+        const float x = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+        o[2 * i] = odd ? x : v[2 * i];
+        o[2 * i + 1] = odd ? v[2 * i + 1] : x;
     }
-    __half *dst = Y + at;
+    if (!in) return;
+    const int first = odd ? 1 : 0;
+    const size_t at = (static_cast<size_t>(m0 + first) * N + (n & ~1)) / 2;  // in pairs
+    uint32_t *dst = reinterpret_cast<uint32_t *>(Y) + at;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i < mrem) dst[static_cast<size_t>(i) * N] = __float2half_rn(v[i]);
+    for (int i = 0; i < 16; ++i) {
+        o[2 * i] += half_lo(rv[i]);
+        o[2 * i + 1] += half_hi(rv[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (2 * i + first < mrem)
+            dst[static_cast<size_t>(i) * N] = pack_half2(o[2 * i], o[2 * i + 1]);
 }
 
 }  // namespace awq

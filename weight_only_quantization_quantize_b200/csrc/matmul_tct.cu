@@ -255,27 +255,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ epilogue
         // lane = output column n0 + col, TMEM column c = token m0 + c; warp
         // half h writes tokens h BT/2 .. (h + 1) BT/2 - 1 of the tile
+        const int c_first = h * (BT / 2), c_end = (h + 1) * (BT / 2);
+        uint32_t rv[16];
+        if constexpr (EPI) epi_load_column32(p.epi, rv, m0 + c_first, p.M - (m0 + c_first), n0 + col, p.N);
         const bool ready = ok && mbar_wait(tmem_full, 0);
         if (__all_sync(0xffffffffu, ready)) {
             tc_fence_after();
             const int n = n0 + col;
             const bool n_in = n < p.N;
+            if constexpr (EPI) {
 #pragma unroll 1
-            for (int c0 = h * (BT / 2); c0 < (h + 1) * (BT / 2); c0 += 32) {
-                const int mrem = p.M - (m0 + c0);  // the same on every lane
-                if (mrem <= 0) break;
-                uint32_t v[32];
-                tmem_ld32(tmem_base + lane_addr + c0, v);
-                if constexpr (EPI) {
+                for (int c0 = c_first; c0 < c_end; c0 += 32) {
+                    const int mrem = p.M - (m0 + c0);  // the same on every lane
+                    if (mrem <= 0) break;
+                    // the next 32 tokens' residual comes in while these are finished
+                    uint32_t next[16];
+                    if (c0 + 32 < c_end) epi_load_column32(p.epi, next, m0 + c0 + 32, mrem - 32, n, p.N);
+                    uint32_t v[32];
+                    tmem_ld32(tmem_base + lane_addr + c0, v);
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(v[i]);
-                    epi_store_column32(p.epi, f, p.Y, m0 + c0, mrem, n, p.N);
-                } else if (n_in) {
-                    __half *dst = p.Y + static_cast<size_t>(m0 + c0) * p.N + n;
+                    epi_store_column32(p.epi, f, rv, p.Y, m0 + c0, mrem, n, p.N);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < mrem) dst[static_cast<size_t>(i) * p.N] = __float2half_rn(__uint_as_float(v[i]));
+                    for (int i = 0; i < 16; ++i) rv[i] = next[i];
+                }
+            } else {
+#pragma unroll 1
+                for (int c0 = h * (BT / 2); c0 < (h + 1) * (BT / 2); c0 += 32) {
+                    const int mrem = p.M - (m0 + c0);  // the same on every lane
+                    if (mrem <= 0) break;
+                    uint32_t v[32];
+                    tmem_ld32(tmem_base + lane_addr + c0, v);
+                    if (n_in) {
+                        __half *dst = p.Y + static_cast<size_t>(m0 + c0) * p.N + n;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i < mrem) dst[static_cast<size_t>(i) * p.N] = __float2half_rn(__uint_as_float(v[i]));
+                    }
                 }
             }
         } else if (lane == 0) {

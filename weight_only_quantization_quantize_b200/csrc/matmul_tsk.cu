@@ -429,6 +429,8 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
                 for (int c0 = h * (BT / 2); c0 < (h + 1) * (BT / 2); c0 += 32) {
                     const int mrem = p.M - (m0 + c0);  // the same on every lane
                     if (mrem <= 0) break;
+                    uint32_t rv[16];
+                    if constexpr (EPI) epi_load_column32(p.epi, rv, m0 + c0, mrem, n, p.N);
                     uint32_t vb[32];
                     tmem_ld32(tmem_base + lane_addr + c0, vb);
                     float v[32];
@@ -457,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
                         add_partials<1>(v, sl, c0, mrem);
                     }
                     if constexpr (EPI) {
-                        epi_store_column32(p.epi, v, p.Y, m0 + c0, mrem, n, p.N);
+                        epi_store_column32(p.epi, v, rv, p.Y, m0 + c0, mrem, n, p.N);
                     } else if (n < p.N) {
                         __half *dst = p.Y + static_cast<size_t>(m0 + c0) * p.N + n;
 #pragma unroll
