@@ -19,7 +19,7 @@
 namespace awq {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kMaxB = AWQ_KV4_MAX_REQUESTS;
 constexpr int kPer = kMaxB / kThreads;  // requests per thread at most
 constexpr size_t kSmemBytes = sizeof(int32_t) * (3 * static_cast<size_t>(kMaxB) + 2);
@@ -139,20 +139,33 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveParams p
     const int64_t stride = static_cast<int64_t>(ranks) * kThreads;
     const int64_t tid = static_cast<int64_t>(rank) * kThreads + threadIdx.x;
     const int tokens = ok ? static_cast<int>(total.a) : 0;
-    for (int64_t t = tid; t < p.T; t += stride) {
-        int64_t slot = -1;
-        int pos = -1;
-        if (t < tokens) {
-            const int b = owner_of(s_cu, p.B, static_cast<int>(t));
-            pos = s_len[b] + static_cast<int>(t) - s_cu[b];
-            const int col = pos >> p.page_shift;
-            const int held = (s_len[b] + P1) >> p.page_shift;
-            const int page = col < held ? p.block_table[static_cast<size_t>(b) * p.max_pages + col]
-                                        : p.free_pages[free0 - 1 - (s_first[b] + col - held)];
-            slot = page < 0 ? -1 : (static_cast<int64_t>(page) << p.page_shift) + (pos & P1);
+    constexpr int kAhead = 4;  // tokens per turn, whose page lookups are in flight together
+    for (int64_t t0 = tid; t0 < p.T; t0 += kAhead * stride) {
+        const int32_t *entry[kAhead];
+        int pos[kAhead], page[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t t = t0 + i * stride;
+            entry[i] = nullptr;
+            pos[i] = -1;
+            if (t < tokens) {
+                const int b = owner_of(s_cu, p.B, static_cast<int>(t));
+                pos[i] = s_len[b] + static_cast<int>(t) - s_cu[b];
+                const int col = pos[i] >> p.page_shift;
+                const int held = (s_len[b] + P1) >> p.page_shift;
+                entry[i] = col < held ? p.block_table + static_cast<size_t>(b) * p.max_pages + col
+                                      : p.free_pages + (free0 - 1 - (s_first[b] + col - held));
+            }
         }
-        p.slots[t] = slot;
-        if (p.positions) p.positions[t] = pos;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) page[i] = entry[i] ? *entry[i] : -1;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t t = t0 + i * stride;
+            if (t >= p.T) break;
+            p.slots[t] = page[i] < 0 ? -1 : (static_cast<int64_t>(page[i]) << p.page_shift) + (pos[i] & P1);
+            if (p.positions) p.positions[t] = pos[i];
+        }
     }
     // the new pages' table entries: read by no thread of this launch
     const int pages = ok ? static_cast<int>(total.b) : 0;
@@ -260,9 +273,9 @@ cudaError_t launch_kv4_reserve(const int32_t *new_lens, const int32_t *lens, int
 {
     const ReserveParams prm{new_lens, lens, free_pages, free_count, block_table, slots, positions, cu, lens_out,
                             free_count_out, status, num_pages, T, B, page_shift, max_pages};
-    // a CTA for each four tokens per thread, up to the portable cluster size
+    // a CTA for each two tokens per thread, up to the portable cluster size
     int ctas = 1;
-    while (ctas < 8 && static_cast<int64_t>(ctas) * kThreads * 4 < T) ctas *= 2;
+    while (ctas < 8 && static_cast<int64_t>(ctas) * kThreads * 2 < T) ctas *= 2;
     const size_t smem = sizeof(int32_t) * (3 * static_cast<size_t>(B) + 2);
     if (ctas == 1) {  // a cluster of its own
         reserve_kernel<<<1, kThreads, smem, st>>>(prm);
