@@ -267,6 +267,16 @@ def test_more_queries_than_cached_tokens_and_empty_requests():
     assert not out[:2].any() and not out[5:9].any()
 
 
+@pytest.mark.parametrize("new", [3, 5, 90])
+def test_windows_over_every_position_are_none(new):
+    # the longest window, and queries that stand before the first token
+    p, c, table = _filled([3], 2, 128, 16, seed=6)
+    q = _rows(new, 8, 128, 1)
+    whole = _check_attention(c, table, q, [0, new], [3], new)
+    for window in (16, 2**31 - 1):
+        assert torch.equal(_check_attention(c, table, q, [0, new], [3], new, window=window), whole)
+
+
 def test_large_and_small_magnitudes():
     # keys and values at both ends of the format: no overflow of weights times steps, no loss to subnormals
     H, D, page = 1, 128, 16

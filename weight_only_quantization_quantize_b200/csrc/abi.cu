@@ -734,7 +734,8 @@ awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, i
     a.T = T;
     a.max_new = static_cast<int>(max_new);
     a.q_heads = static_cast<int>(q_heads);
-    a.window = static_cast<int>(window);
+    // a window over every position of the table is none (and position - window stays an int)
+    a.window = window >= max_pages * page_size ? 0 : static_cast<int>(window);
     a.scale = scale;
     a.status = dev_status;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
