@@ -436,7 +436,9 @@ AWQ_API awq_status_t awq_kv4_reserve(const int32_t *new_lens, const int32_t *len
  * and the table entries of those pages -1.
  *   done int32 [B]; lens, block_table, free_pages, free_count updated in place
  * Device errors: AWQ_ERR_RANGE (a length or page out of range, more pages than
- * num_pages in the stack); then nothing is changed.
+ * num_pages in the stack); then nothing is changed.  Every page of an ended
+ * request has to be in its row, and in no other request's: a page that two rows
+ * share would be pushed twice, which is not detected.
  */
 AWQ_API awq_status_t awq_kv4_release(const int32_t *done, int32_t *lens, int64_t B, int64_t page_size,
                                      int32_t *block_table, int64_t max_pages, int32_t *free_pages,
@@ -480,10 +482,13 @@ AWQ_API awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_he
  *   out = sum_j softmax_j(scale * q . k_j) v_j
  * in float, over the values the codes stand for, rounded once to binary16; a
  * query that sees nothing gives zeros.  Query head h reads key/value head
- * h / (q_heads / kv_heads).
+ * h / (q_heads / kv_heads).  Pages that lie wholly before the window of a
+ * request's first query are not looked at: their table entries may be -1.
+ * Requests of one call may differ in n_b: those with many query rows and those
+ * with few go to two kernels, one after the other.
  *   q       binary16, row t at q + t * q_stride (elements, a multiple of 8,
  *           >= q_heads * D)
- *   cu      int32 [B + 1], or NULL: one query per request (T >= B)
+ *   cu      int32 [B + 1], ascending, or NULL: one query per request (T >= B)
  *   max_new the most queries of one request (a bound known on the host)
  *   out     binary16 [T, q_heads, D] (output); rows of no request are not written
  *   workspace  at least awq_kv4_attention_workspace_size(D) bytes, no initial

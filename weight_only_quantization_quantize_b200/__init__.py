@@ -644,7 +644,8 @@ class KV4Pages:
     num_pages pages of page_size tokens (16, 32, 64, 128 or 256); max_requests rows of at most max_pages
     pages.  State on the device, all int32: block_table [max_requests, max_pages], lens [max_requests],
     free_pages [num_pages] with free_count [1] (a stack).  Given tensors are used as they are; by default every page is
-    free."""
+    free.  The state tensors may be written at any time but not replaced: calls and captured graphs keep their
+    addresses."""
 
     def __init__(self, num_pages, page_size, max_requests, max_pages, device="cuda", block_table=None, lens=None,
                  free_pages=None, free_count=None):
@@ -715,7 +716,9 @@ class KV4Pages:
         return slots, positions, cu
 
     def release(self, done, status=None):
-        """Ends the requests with done[b] != 0 (int32 [max_requests]): their pages return to the stack."""
+        """Ends the requests with done[b] != 0 (int32 [max_requests]): their pages return to the stack.
+
+        Every page of such a request must be in its row of the table and in no other request's."""
         dev = self.device
         _match(done, torch.int32, (self.max_requests,), "done", dev)
         if status is not None:
@@ -727,7 +730,8 @@ class KV4Pages:
 class KV4Cache:
     """Keys and values of one layer in 4 bits, on the pages of a KV4Pages.
 
-    data: uint8 [num_pages, kv_heads, kv4_page_bytes(page_size, head_dim)] (default: a zeroed one)."""
+    data: uint8 [num_pages, kv_heads, kv4_page_bytes(page_size, head_dim)] (default: a zeroed one);
+    like the state of the pages it is updated in place, never replaced."""
 
     def __init__(self, pages: KV4Pages, kv_heads: int, head_dim: int, data=None):
         if not 1 <= kv_heads <= 1024:
@@ -811,7 +815,7 @@ class KV4Cache:
 
         cu: int32 [max_requests + 1], the query rows of each request (from reserve); None: one query per request.
         max_new: the most queries of one request.  scale: default head_dim ** -0.5.
-        window: positions seen, 0 for all.  Returns [T, q_heads, head_dim]; rows of no request are not written.
+        window: positions seen, 0 for all; pages wholly before it may be gone from the table (-1).  Returns [T, q_heads, head_dim]; rows of no request are not written.
         workspace: uint8 of kv4_attention_workspace_size(head_dim) bytes; by default the stream's cached one, or the
         graph's own during capture."""
         p = self.pages
