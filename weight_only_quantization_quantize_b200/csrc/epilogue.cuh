@@ -78,13 +78,32 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
 __device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w))); }
 __device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half(static_cast<uint16_t>(w >> 16))); }
 
-// Eight consecutive columns n .. n + 7 of token `tok` (N columns before the
-// gate): finish and write them, 16 bytes, or 8 bytes when gated.
-__device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __half *Y, int tok, int n, int N)
+// What columns n .. n + 7 of token `tok` (N columns before the gate) need
+// besides their sums; zeros where the call has none.
+struct Epi8 {
+    uint4 bias, residual;  // gated: four residuals, in x and y
+};
+
+__device__ __forceinline__ Epi8 epi_load8(const Epilogue &e, int tok, int n, int N)
+{
+    Epi8 x{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (e.bias) x.bias = *reinterpret_cast<const uint4 *>(e.bias + n);
+    if (e.residual && e.gated) {
+        const uint2 r = *reinterpret_cast<const uint2 *>(e.residual + static_cast<size_t>(tok) * (N / 2) + n / 2);
+        x.residual.x = r.x;
+        x.residual.y = r.y;
+    } else if (e.residual) {
+        x.residual = *reinterpret_cast<const uint4 *>(e.residual + static_cast<size_t>(tok) * N + n);
+    }
+    return x;
+}
+
+// Finishes and writes those eight columns, 16 bytes, or 8 bytes when gated.
+__device__ __forceinline__ void epi_store8(const Epilogue &e, const Epi8 &x, float (&v)[8], __half *Y, int tok, int n,
+                                           int N)
 {
     if (e.bias) {
-        const uint4 b = *reinterpret_cast<const uint4 *>(e.bias + n);
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+        const uint32_t w[4] = {x.bias.x, x.bias.y, x.bias.z, x.bias.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] += half_lo(w[i]);
@@ -98,7 +117,7 @@ __device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __h
         });
         const size_t at = static_cast<size_t>(tok) * (N / 2) + n / 2;
         if (e.residual) {
-            const uint2 r = *reinterpret_cast<const uint2 *>(e.residual + at);
+            const uint4 r = x.residual;
             v[0] += half_lo(r.x); v[1] += half_hi(r.x); v[2] += half_lo(r.y); v[3] += half_hi(r.y);
         }
         *reinterpret_cast<uint2 *>(Y + at) = make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
@@ -110,8 +129,7 @@ __device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __h
     });
     const size_t at = static_cast<size_t>(tok) * N + n;
     if (e.residual) {
-        const uint4 r = *reinterpret_cast<const uint4 *>(e.residual + at);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+        const uint32_t w[4] = {x.residual.x, x.residual.y, x.residual.z, x.residual.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] += half_lo(w[i]);
@@ -120,6 +138,11 @@ __device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __h
     }
     *reinterpret_cast<uint4 *>(Y + at) = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]),
                                                     pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void epi_store8(const Epilogue &e, float (&v)[8], __half *Y, int tok, int n, int N)
+{
+    epi_store8(e, epi_load8(e, tok, n, N), v, Y, tok, n, N);
 }
 
 // The residual of token `tok`, columns n0 .. n0 + 127 before the gate, on its way

@@ -431,14 +431,23 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
     // byte pushed to it before it reduces, so no push into a CTA is in flight
     // when that CTA leaves.  (A release here fenced on the pushes' completion.)
     cluster_arrive_relaxed();
+    // A thread finishes one chunk at most (M <= 2, 16 chunks): its bias and
+    // residual are on their way while the partials arrive (1 x 14336 x 4096 with a
+    // residual: 11.9 us when read behind them, 9.4 so, 8.8 without an epilogue).
+    const int lchunks = cpo / 8;
+    Epi8 around{};
+    if constexpr (EPI) {
+        pdl_wait();  // every thread may read the residual
+        const int tok = static_cast<int>(threadIdx.x) / lchunks;
+        const int n = n0 + ((static_cast<int>(threadIdx.x) - tok * lchunks) * p.splits + split) * 8;
+        if (tok < p.M && n < p.N) around = epi_load8(p.epi, tok, n, p.N);
+    }
     // Reduce the columns this rank owns, partials summed in (rank, k-half) order.
     if (!mbar_wait(recv_bar, 0)) {
         if (threadIdx.x == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
         // the partials pushed into this CTA still land before it exits
         mbar_wait_for(recv_bar, 0, kDrainLimitNs);
     }
-    if constexpr (EPI) pdl_wait();  // every thread may read the residual
-    const int lchunks = cpo / 8;
     for (int e = threadIdx.x; e < p.M * lchunks; e += kAllThreads) {
         const int tok = e / lchunks;
         const int lch = e - tok * lchunks;
@@ -454,7 +463,7 @@ __global__ void __launch_bounds__(32 * (kConsumers + 1), 1)
             v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
         }
         if constexpr (EPI) {
-            epi_store8(p.epi, v, p.Y, tok, n, p.N);
+            epi_store8(p.epi, around, v, p.Y, tok, n, p.N);
             continue;
         }
         uint4 o;
