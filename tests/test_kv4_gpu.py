@@ -558,3 +558,23 @@ def test_pages_before_the_window_may_be_gone(new):
         p.block_table[0, :gone] = -1
         q = _rows(2 * new, 8, 64, 5)
         _check_attention(c, table, q, [0, new, 2 * new], [n, 3 * page], new, window=window)
+
+
+@pytest.mark.parametrize("fill", [0xFF, 0x80, 0x7F, 0x00])
+@pytest.mark.parametrize("lens,new,window", [([4000, 900], [300, 90], 60), ([4000, 900], [300, 90], 0), ([2000, 33, 512], [60, 1, 12], 0),
+                                             ([900, 4000], [1, 1], 0)])
+def test_workspaces_may_hold_anything(lens, new, window, fill):
+    # the grid of a prompt call is a bound on its row blocks: those that no request has are skipped, whatever the
+    # workspace held where they would stand
+    p, c, table = _filled(lens, 4, 128, 64, seed=sum(lens))
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = _rows(cu[-1], 8, 128, 23)
+    around = torch.full((3, cu[-1], 8, 128), 7.0, dtype=torch.float16, device="cuda")
+    ws = torch.full((awq.kv4_attention_workspace_size(128),), fill, dtype=torch.uint8, device="cuda")
+    st = awq.new_status("cuda")
+    out = c.attention(q.cuda(), cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), max_new=max(new), window=window,
+                      out=around[1], status=st, workspace=ws)
+    awq.raise_on_status(st)
+    want, bound = ref.attention(q, _bytes(c.data), table.numpy(), lens, cu, 64, 128 ** -0.5, window)
+    assert bool(((out.cpu().double() - want).abs() <= bound).all())
+    assert bool((around[0] == 7.0).all()) and bool((around[2] == 7.0).all())

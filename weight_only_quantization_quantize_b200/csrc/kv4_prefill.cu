@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
     }
     const int b = s_request;
     if (b < 0) {
-        if (p.splits > 1 && head == 0 && split == 0 && threadIdx.x == 0) p.rows[flat].rows = 0;
+        // every field: the join adds to `first` before it compares with `rows`, and the workspace may hold anything
+        if (p.splits > 1 && head == 0 && split == 0 && threadIdx.x == 0) p.rows[flat] = BlockRows{0, 0, 0, 0};
         return;
     }
     const int rb = s_block;
