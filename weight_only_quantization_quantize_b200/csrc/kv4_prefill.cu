@@ -537,9 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                     // the half that has just failed goes on to its maximum
                     if (!ready || (clear && h == from) || weights(std::true_type{}, h)) ok = masked_half(64 * h) && ok;
                 }
+                if (!ok) break;  // nothing is handed on: the issuer's own wait ends it
                 publish(1);
                 if (lane == 0) mbar_arrive(&bars.k_empty[st]);
-                if (!ok) break;
                 if (!ready) ready = __all_sync(0xffffffffu, m != -INFINITY);
             }
             // -------------------------------------------------------- output
@@ -752,12 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const Params p)
                 }
                 if (ok && j + 1 < tiles) tc_commit(&bars.k_empty[sn]);
             }
-            if (!ok) {
-                // every MMA issued completes before tensor memory is freed
-                report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
-                tc_commit(&bars.drain);
-                mbar_wait_for(&bars.drain, 0, kDrainLimitNs);
-            }
+            if (!ok) report(a.status, AWQ_ERR_DEVICE_TIMEOUT);
+            // Every MMA issued completes, and every commit has arrived, before tensor
+            // memory is freed and the CTA leaves, whichever role's wait ran out (the
+            // softmax warps skip the outputs' barrier after one of theirs).  Otherwise it
+            // passes with that barrier.
+            tc_commit(&bars.drain);
+            mbar_wait_for(&bars.drain, 0, kDrainLimitNs);
         }
     }
     __syncwarp();
