@@ -171,12 +171,14 @@ __global__ void __launch_bounds__(160, 1)
         // the X' boxes hold 8 MT token rows (rows at and beyond M read as zero)
         const uint32_t tx = kQStage + 2 * (8 * MT) * 128;
         bool ok = true;
+        int issued = 0;
         for (int it = 0; it < ng; ++it) {
             const int st = it % S;
             if (it >= S && !mbar_wait(&empty[st], ((it / S) - 1) & 1)) {
                 ok = false;
                 break;
             }
+            issued = it + 1;
             uint8_t *stg = smem + st * p.stage_bytes;
             const int g = g_begin + it;
             if (lane == 0) {
@@ -189,6 +191,11 @@ __global__ void __launch_bounds__(160, 1)
             }
         }
         if (!ok && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        // The copies issued land before the CTA can exit, whichever warp's wait ran out.
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (lane == 0)
+            for (int it = issued > S ? issued - S : 0; it < issued; ++it)
+                mbar_wait_for(&full[it % S], (it / S) & 1, kDrainLimitNs);
     } else {
         // ------------------------------------------------------------ consumers
         const int gq = lane >> 2;
@@ -336,7 +343,11 @@ __global__ void __launch_bounds__(160, 1)
     // Arrive once the pushes are issued (no fence: every owner waits for all
     // the bytes pushed to it before it reduces, hence before it exits).
     cluster_arrive_relaxed();
-    if (!mbar_wait(recv_bar, 0) && threadIdx.x == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+    if (!mbar_wait(recv_bar, 0)) {
+        if (threadIdx.x == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        // the partials pushed into this CTA still land before it exits
+        mbar_wait_for(recv_bar, 0, kDrainLimitNs);
+    }
     if constexpr (EPI) pdl_wait();  // every thread may read the residual
     const int lchunks = cpo / 8;
     for (int e = threadIdx.x; e < p.M * lchunks; e += kAllThreads) {

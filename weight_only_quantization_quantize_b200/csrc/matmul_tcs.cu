@@ -142,10 +142,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&tmQ);
         }
         pdl_wait();  // X' comes from the pre-pass kernel
+        int issued = 0;
         for (int i = 0; i < nkb; ++i) {
             const int kb = kb_begin + i;
             const int st = i % kLoadStages;
-            if (i >= kLoadStages && !mbar_wait(&empty_load[st], ((i / kLoadStages) - 1) & 1)) {
+            const bool w = i < kLoadStages || mbar_wait(&empty_load[st], ((i / kLoadStages) - 1) & 1);
+            if (!__all_sync(0xffffffffu, w)) {
                 ok = false;
                 break;
             }
@@ -169,9 +171,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                            zero_word_src(p.zeros, g, p.N / 8, in ? wi : 0, lane), in ? 4u : 0u);
             }
             cp_async_arrive_noinc(&full_load[st]);
+            ++issued;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
         if (!ok && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        // The copies issued land before the ring takes the pushed partials and the CTA
+        // can exit, whichever warp's wait ran out.
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (lane == 0)
+            for (int i = issued > kLoadStages ? issued - kLoadStages : 0; i < issued; ++i)
+                mbar_wait_for(&full_load[i % kLoadStages], (i / kLoadStages) & 1, kDrainLimitNs);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc = tc_idesc_f16(kBN, p.nt);
@@ -198,13 +206,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
         if (lane == 0) {
-            // tmem_full completes once every MMA issued has completed; after a
-            // timeout this lane waits for that itself before TMEM is freed
+            // tmem_full completes once every MMA issued has completed; this lane
+            // waits for that itself before TMEM is freed, because a consumer's wait
+            // for it may have run out
             tc_commit(tmem_full);
-            if (!ok) {
-                report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
-                mbar_wait_for(tmem_full, 0, kDrainLimitNs);
-            }
+            if (!ok) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+            mbar_wait_for(tmem_full, 0, kDrainLimitNs);
         }
         __syncwarp();
     } else {
@@ -290,7 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Arrive once the pushes are issued (no fence: every owner waits for all
     // the bytes pushed to it before it reduces, hence before it exits).
     cluster_arrive_relaxed();
-    if (!mbar_wait(recv_bar, 0) && threadIdx.x == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+    if (!mbar_wait(recv_bar, 0)) {
+        if (threadIdx.x == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        // the partials pushed into this CTA still land before it exits
+        mbar_wait_for(recv_bar, 0, kDrainLimitNs);
+    }
     if constexpr (EPI) {
         // columns in pairs (2j, 2j + 1): a gate and its column sit in one thread
         pdl_wait();  // every thread may read the residual

@@ -156,15 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             cp_async_arrive_noinc(&full_load[st]);
             ++issued;
         }
-        if (!ok) {
-            // let the copies already issued land before the CTA exits
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            if (lane == 0) {
-                report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
-                const int first = issued > kLoadStages ? issued - kLoadStages : 0;
-                for (int it = first; it < issued; ++it)
-                    mbar_wait_for(&full_load[it % kLoadStages], (it / kLoadStages) & 1, kDrainLimitNs);
-            }
+        // The copies issued land before the CTA can exit, whichever warp's wait ran
+        // out: after a consumer's did, this one may have nothing to wait for itself.
+        if (!ok && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (lane == 0) {
+            const int first = issued > kLoadStages ? issued - kLoadStages : 0;
+            for (int it = first; it < issued; ++it)
+                mbar_wait_for(&full_load[it % kLoadStages], (it / kLoadStages) & 1, kDrainLimitNs);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -193,13 +192,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
         if (lane == 0) {
-            // tmem_full completes when every MMA issued has completed; on a
-            // timeout this lane waits for that itself before TMEM is freed
+            // tmem_full completes when every MMA issued has completed; this lane
+            // waits for that itself before TMEM is freed, because a consumer's wait
+            // for it may have run out
             tc_commit(tmem_full);
-            if (!ok) {
-                report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
-                mbar_wait_for(tmem_full, 0, kDrainLimitNs);
-            }
+            if (!ok) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+            mbar_wait_for(tmem_full, 0, kDrainLimitNs);
         }
         __syncwarp();
     } else {

@@ -253,15 +253,14 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
             }
             u += sg.s1 - sg.s0;
         }
-        if (!ok) {
-            // let the copies already issued land before the CTA exits
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            if (lane == 0) {
-                report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
-                const int first = it > C::kStages ? it - C::kStages : 0;
-                for (int j = first; j < it; ++j)
-                    mbar_wait_for(&full_load[j % C::kStages], (j / C::kStages) & 1, kDrainLimitNs);
-            }
+        // The copies issued land before the CTA can exit, whichever warp's wait ran
+        // out: after a consumer's did, this one may have nothing to wait for itself.
+        if (!ok && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (lane == 0) {
+            const int first = it > C::kStages ? it - C::kStages : 0;
+            for (int j = first; j < it; ++j)
+                mbar_wait_for(&full_load[j % C::kStages], (j / C::kStages) & 1, kDrainLimitNs);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -306,9 +305,10 @@ __global__ void __launch_bounds__(kThreads, BT == 128 ? 2 : 1)
             __syncwarp();
             u += sg.s1 - sg.s0;
         }
-        if (!ok && lane == 0) {
-            // every MMA issued completes before tensor memory is freed
-            report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        if (lane == 0) {
+            // every MMA issued completes before tensor memory is freed, also when
+            // only a consumer's wait for it ran out
+            if (!ok) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
             tc_commit(drain);
             mbar_wait_for(drain, 0, kDrainLimitNs);
         }

@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kDThreads, 1)
         if (lane == 0) {
             prefetch_tmap(&tmX);
             prefetch_tmap(&tmWT);
+            int issued = 0;
             for (int kb = 0; kb < KB; ++kb) {
                 const int st = kb % kDStages;
                 if (kb >= kDStages && !mbar_wait(&empty[st], ((kb / kDStages) - 1) & 1)) {
@@ -200,13 +201,17 @@ __global__ void __launch_bounds__(kDThreads, 1)
                 mbar_arrive_expect_tx(&full[st], kDStageBytes);
                 tma_load_2d(stg, &tmX, &full[st], kb * kDBK, m0);
                 tma_load_2d(stg + kDABytes, &tmWT, &full[st], kb * kDBK, n0);
+                ++issued;
             }
             if (!ok) report(status, AWQ_ERR_DEVICE_TIMEOUT);
+            // the copies issued land before the CTA can exit, whichever warp's wait ran out
+            for (int it = issued > kDStages ? issued - kDStages : 0; it < issued; ++it)
+                mbar_wait_for(&full[it % kDStages], (it / kDStages) & 1, kDrainLimitNs);
         }
     } else if (warp == 1) {
         for (int kb = 0; kb < KB; ++kb) {
             const int st = kb % kDStages;
-            if (!mbar_wait(&full[st], (kb / kDStages) & 1)) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (kb / kDStages) & 1))) {
                 ok = false;
                 break;
             }
@@ -223,14 +228,15 @@ __global__ void __launch_bounds__(kDThreads, 1)
             __syncwarp();
         }
         if (lane == 0) {
-            if (ok)
-                tc_commit(tmem_full);
-            else
-                report(status, AWQ_ERR_DEVICE_TIMEOUT);
+            // tmem_full completes when every MMA issued has completed: before tensor
+            // memory is freed, whichever wait ran out
+            tc_commit(tmem_full);
+            if (!ok) report(status, AWQ_ERR_DEVICE_TIMEOUT);
+            mbar_wait_for(tmem_full, 0, kDrainLimitNs);
         }
         __syncwarp();
     } else {
-        if (mbar_wait(tmem_full, 0)) {
+        if (__all_sync(0xffffffffu, mbar_wait(tmem_full, 0))) {
             tc_fence_after();
             const int quarter = warp & 3;
             const int m = m0 + quarter * 32 + lane;
@@ -252,9 +258,6 @@ __global__ void __launch_bounds__(kDThreads, 1)
             report(status, AWQ_ERR_DEVICE_TIMEOUT);
         }
     }
-    // a producer that gave up may have copies in flight: let them land
-    if (warp == 0 && lane == 0 && !ok)
-        for (int st = 0; st < kDStages; ++st) mbar_wait(&full[st], 0);
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
