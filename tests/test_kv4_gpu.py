@@ -578,3 +578,28 @@ def test_workspaces_may_hold_anything(lens, new, window, fill):
     want, bound = ref.attention(q, _bytes(c.data), table.numpy(), lens, cu, 64, 128 ** -0.5, window)
     assert bool(((out.cpu().double() - want).abs() <= bound).all())
     assert bool((around[0] == 7.0).all()) and bool((around[2] == 7.0).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("lens,new,max_pages", [
+    ([40, 1, 300], [1, 1, 1], None), ([77, 9], [6, 3], None),          # few rows
+    ([200, 90], [120, 40], None), ([300, 2], [300, 30], None),         # prompts, keys in one piece; queries before the first token
+    ([1500, 700], [70, 33], 64), ([4000, 3], [90, 60], 64)])           # prompts whose keys are split
+def test_queries_that_are_not_finite_show(bad, lens, new, max_pages):
+    # an overflow upstream reaches the output of its own rows on every path, and no other row
+    p, c, table = _filled(lens, 2, 128, 64, seed=sum(lens), max_pages=max_pages)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    clean = _rows(cu[-1], 8, 128, 29)
+    want, bound = ref.attention(clean, _bytes(c.data), table.numpy(), lens, cu, 64, 128 ** -0.5)
+    hit = torch.zeros(cu[-1], 8, dtype=torch.bool)
+    for b in range(len(lens)):
+        hit[cu[b], 3] = hit[cu[b + 1] - 1, 6] = True
+    q = clean.clone()
+    q[..., 5][hit] = bad
+    st = awq.new_status("cuda")
+    out = c.attention(q.cuda(), cu=torch.tensor(cu, dtype=torch.int32, device="cuda"), max_new=max(new), status=st).cpu().double()
+    awq.raise_on_status(st)
+    sees = torch.cat([torch.arange(n - m, n) >= 0 for n, m in zip(lens, new)])
+    gone = hit & sees[:, None]
+    assert bool(out[gone].isnan().all())
+    assert bool(((out - want).abs() <= bound)[~gone].all())

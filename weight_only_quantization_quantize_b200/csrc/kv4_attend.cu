@@ -359,9 +359,11 @@ __device__ __forceinline__ void tile_step(Warp<D, WT> &w, const uint8_t *stage, 
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        // select, never multiply: what a masked place holds may be anything
+                        // select, never multiply: what a masked place holds may be anything; a
+                        // product that is not finite (x - x is then NaN) is not taken for one
                         const bool seen = full || (there && j <= w.hi[n][c] && j > w.lo[n][c]);
-                        s[b][n][2 * h + c] = seen ? f[b][h] * s[b][n][2 * h + c] : -INFINITY;
+                        const float x = s[b][n][2 * h + c];
+                        s[b][n][2 * h + c] = seen ? fmaf(f[b][h], x, x - x) : -INFINITY;
                     }
             }
 #pragma unroll

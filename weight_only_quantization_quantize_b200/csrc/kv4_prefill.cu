@@ -795,8 +795,11 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p)
 #pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
         const float2 ml = p.ml[slot(s)];
-        if (ml.x == -INFINITY) continue;  // saw no key: its numerators may not be written
-        const float f = ex2(ml.x - top);
+        // A part that saw no key has the sum 0, and its numerators may not be written.  (A
+        // row of NaN logits has no reference either, but a sum of NaN, which has to reach
+        // the output.)
+        if (ml.y == 0.0f) continue;
+        const float f = ex2(ml.x - top);  // NaN for a row without a reference: like its sum
         l += ml.y * f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += p.part[slot(s) * D + E * lane + e] * f;
