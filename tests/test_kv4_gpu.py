@@ -603,3 +603,21 @@ def test_queries_that_are_not_finite_show(bad, lens, new, max_pages):
     gone = hit & sees[:, None]
     assert bool(out[gone].isnan().all())
     assert bool(((out - want).abs() <= bound)[~gone].all())
+
+
+@pytest.mark.parametrize("written", [0, 1, 40])
+@pytest.mark.parametrize("m,max_pages", [(1, None), (100, None), (100, 64)])
+def test_whole_tiles_of_stored_zeros(written, m, max_pages):
+    # runs of slots that were never written, longer than a key tile, before and between written ones
+    n, page = 700, 64
+    p, c, table = _filled([n], 1, 128, page, seed=5, poison=False, max_pages=max_pages)
+    c.data.zero_()
+    at = torch.arange(written) * 11 + 230
+    k = _rows(written, 1, 128, 3)
+    if written:
+        c.append(k.cuda(), k.cuda(), (table[0].long()[at // page] * page + at % page).cuda())
+    q = _rows(m, 2, 128, 1)
+    out = _check_attention(c, table, q, [0, m], [n], m)
+    if not written:
+        assert not out.any()
+    _check_attention(c, table, q, [0, m], [n], m, window=150)

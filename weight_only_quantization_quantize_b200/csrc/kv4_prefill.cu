@@ -187,10 +187,12 @@ struct Bars {
     uint64_t q_full[2], s_full[2], p_half[2][2], pv_half[2], o_full[2], drain;
 };
 
-// An upper bound of log2(step), at most 1 above it (steps are normal floats, or 0).
+// An upper bound of log2(step), at most 1 above it, and that of the smallest step for
+// 0 (a slot never written): without the floor a reference of 2^-126 would make
+// the weights of such keys infinite.  (Binary16 steps are normal floats, or 0.)
 __device__ __forceinline__ float step_log2(float step)
 {
-    return static_cast<float>(static_cast<int>(__float_as_uint(step) >> 23) - 126);
+    return static_cast<float>(max(static_cast<int>(__float_as_uint(step) >> 23) - 126, -23));
 }
 
 template <int N>
