@@ -402,6 +402,8 @@ AWQ_API awq_status_t awq_w4a16_gemm_epilogue(const uint16_t *X, const uint16_t *
 #define AWQ_KV4_BLOCK 16
 #define AWQ_KV4_MAX_REQUESTS 4096
 #define AWQ_KV4_MAX_HEADS 1024      /* query heads; key/value heads likewise */
+#define AWQ_KV4_MAX_PAIRS ((int64_t)1 << 52) /* query rows x positions of one request and
+                                       key/value head: close to an hour of GPU time */
 
 /* Bytes of one page for one head; 0 for an unsupported page_size or D. */
 AWQ_API size_t awq_kv4_page_bytes(int64_t page_size, int64_t D);
@@ -495,9 +497,11 @@ AWQ_API awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_he
  *           contents required, overwritten; calls that can run at the same time
  *           need separate ones
  *   q_heads % kv_heads == 0, both <= AWQ_KV4_MAX_HEADS; 1 <= B <=
- *   AWQ_KV4_MAX_REQUESTS; 1 <= T, max_new < 2^31; max_pages * page_size < 2^31;
- *   B * kv_heads * ceil(max_new * q_heads / kv_heads / 8) * (max_pages * page_size /
- *   32 + 4) < 2^32
+ *   AWQ_KV4_MAX_REQUESTS; 1 <= T, max_new < 2^31; tokens = max_pages * page_size < 2^31;
+ *   with rows = max_new * q_heads / kv_heads (requests of more than 48 rows go to the
+ *   kernel for many rows, so that more count as 48 in the first):
+ *   B * kv_heads * (rows <= 8 ? 1 : ceil(min(rows, 48) / 16)) * (ceil(tokens / 64) + 8) < 2^32,
+ *   rows * tokens <= AWQ_KV4_MAX_PAIRS
  * The result depends on the number of SMs and on the bounds max_new, max_pages
  * and T (which choose the kernel and the order of sums), never on timing: the
  * same call gives the same bits.

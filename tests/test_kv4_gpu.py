@@ -621,3 +621,31 @@ def test_whole_tiles_of_stored_zeros(written, m, max_pages):
     if not written:
         assert not out.any()
     _check_attention(c, table, q, [0, m], [n], m, window=150)
+
+
+@pytest.mark.parametrize("m", [1, 3, 60])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_infinite_logits_of_a_single_key_show(m, bad):
+    # one cached token whose codes make the infinite query's logit -inf in one head and +inf in the other
+    p, c, table = _filled([1], 1, 64, 16, seed=1)
+    k = torch.zeros(1, 1, 64, dtype=torch.float16)
+    k[..., 5], k[..., 9] = -2.0, 2.0
+    c.append(k.cuda(), torch.ones_like(k).cuda(), (table[0, :1].long() * 16).cuda())
+    q = _rows(m, 2, 64, 1)
+    q[-1, 0, 5] = q[-1, 1, 9] = bad
+    st = awq.new_status("cuda")
+    out = c.attention(q.cuda(), cu=torch.tensor([0, m], dtype=torch.int32, device="cuda"), max_new=m, status=st)
+    awq.raise_on_status(st)
+    assert bool(out[-1].isnan().all()) and not out[:-1].any()   # the earlier queries stand before the first token
+
+
+def test_wide_tables_and_long_chunks():
+    # the bounds of a server: 256 rows of 65536 tokens, a chunk of up to 2048 tokens among single ones
+    B, Hk, D, page = 256, 8, 64, 16
+    lens = [33 + i % 40 for i in range(B)]
+    new = [1] * B
+    new[7], lens[7] = 130, 700
+    new[100] = 0
+    p, c, table = _filled(lens, Hk, D, page, seed=3, max_pages=4096)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    _check_attention(c, table, _rows(cu[-1], 32, D, 5), cu, lens, 2048)

@@ -114,3 +114,26 @@ def test_host_tensors_are_refused():
         awq.KV4Pages(4, 16, 1, 4, block_table=torch.zeros(1, 4, dtype=torch.int32))
     with pytest.raises(TypeError, match="CUDA"):
         awq.w4a16_gemm_epilogue(torch.zeros(1, 128, dtype=torch.float16), None, None, None, None)
+
+
+def test_attention_takes_serving_bounds(L):
+    # shapes are judged before the workspace: a missing one shows that the bounds were taken
+    def call(B, H, Hk, tokens, mn, page=16, D=128):
+        return L.awq_kv4_attention(P(A), H * D, 1 << 20, H, P(A), 1 << 20, page, Hk, D, P(A), tokens // page, P(A), P(A), B, mn,
+                                   0.1, 0, P(A), None, 0, None, None)
+    for B, H, Hk, tokens, mn in ((256, 32, 8, 65536, 2048), (64, 32, 8, 131072, 4096), (8, 64, 64, 131072, 32768),
+                                 (8, 64, 8, 131072, 32768), (4096, 64, 8, 131072, 131072), (1, 64, 1, 1 << 24, 1 << 20),
+                                 (4096, 8, 8, 1 << 20, 1)):
+        assert call(B, H, Hk, tokens, mn) == awq.ERR_WORKSPACE, (B, H, Hk, tokens, mn)
+    # one item of a one-page table is 9 units (a tile, and what an item costs besides): 4096 * 1024 * 9 stays below
+    # 2^32, 4096 * 1024 * (2^16 / 64 + 8) does not
+    assert call(4096, 1024, 1024, 16, 1) == awq.ERR_WORKSPACE
+    assert call(4096, 1024, 1024, 1 << 16, 1) == awq.ERR_SHAPE
+    # the limit itself: 4096 * 64 * (tokens / 64 + 8) against 2^32, items of 8 rows, then three of 16
+    assert call(4096, 64, 64, 64 * (16384 - 9), 8) == awq.ERR_WORKSPACE
+    assert call(4096, 64, 64, 64 * (16384 - 8), 8) == awq.ERR_SHAPE
+    assert call(4096, 64, 64, 64 * 5453, 33) == awq.ERR_WORKSPACE
+    assert call(4096, 64, 64, 64 * 5454, 33) == awq.ERR_SHAPE
+    # more than 2^52 query rows times positions
+    assert call(1, 8, 2, 1 << 30, 1 << 20) == awq.ERR_WORKSPACE
+    assert call(1, 8, 2, 1 << 30, (1 << 20) + 1) == awq.ERR_SHAPE

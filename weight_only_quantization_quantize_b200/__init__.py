@@ -815,7 +815,10 @@ class KV4Cache:
 
         cu: int32 [max_requests + 1], the query rows of each request (from reserve); None: one query per request.
         max_new: the most queries of one request.  scale: default head_dim ** -0.5.
-        window: positions seen, 0 for all; pages wholly before it may be gone from the table (-1).  Returns [T, q_heads, head_dim]; rows of no request are not written.
+        window: positions seen, 0 for all; pages wholly before it may be gone from the table (-1).
+        Returns [T, q_heads, head_dim]; rows of no request are not written.
+        AwqError (ERR_SHAPE) for bounds whose work is not counted in 32 bits: max_requests * kv_heads *
+        (1 to 3, by rows of a request) * (max_pages * page_size / 64 + 8) has to stay below 2**32.
         workspace: uint8 of kv4_attention_workspace_size(head_dim) bytes; by default the stream's cached one, or the
         graph's own during capture."""
         p = self.pages

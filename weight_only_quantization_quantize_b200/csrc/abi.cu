@@ -713,10 +713,11 @@ awq_status_t awq_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t T, i
         q_stride < q_heads * D || q_stride > INT32_MAX || max_new < 1 || max_new > INT32_MAX || window < 0 ||
         window > INT32_MAX || (!cu && T < B))
         return AWQ_ERR_SHAPE;
-    // the run of tiles that the kernel splits is counted in 32 bits
-    const int64_t blocks = (max_new * (q_heads / kv_heads) + 7) / 8;
-    const int64_t tiles = max_pages * page_size / 32 + 4;
-    if (blocks > (int64_t(1) << 32) / (B * kv_heads) / tiles) return AWQ_ERR_SHAPE;
+    // the few-row kernel, whose requests have at most kPromptRows rows, counts its tiles in 32 bits
+    const int64_t rows = max_new * (q_heads / kv_heads), tokens = max_pages * page_size;
+    if (!awq::kv4_attend_countable(B, kv_heads, rows < awq::kPromptRows ? rows : awq::kPromptRows, tokens) ||
+        rows > AWQ_KV4_MAX_PAIRS / tokens)
+        return AWQ_ERR_SHAPE;
     if (!aligned16(q) || q_stride % 8 || !aligned16(cache) || !aligned4(block_table) || !aligned4(lens) ||
         (cu && !aligned4(cu)) || !aligned16(out) || (workspace && !aligned16(workspace)) ||
         (dev_status && !aligned4(dev_status)))

@@ -71,6 +71,9 @@ struct Kv4AttendArgs {
 // 57 / 49 and 156 / 100 (32 x 4000); 128 rows 94 / 51.
 constexpr int kPromptRows = 48;
 cudaError_t configure_kv4_attend();
+// Whether the longest line of tiles that B requests of at most `rows` rows and `tokens` cached tokens can make
+// is counted in 32 bits.
+bool kv4_attend_countable(int64_t B, int64_t heads, int64_t rows, int64_t tokens);
 size_t kv4_attend_workspace(int D);
 // requests with more than max_rows rows are left to the prompt kernel
 cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, int64_t max_rows, void *ws, int num_sms, cudaStream_t st);

@@ -467,7 +467,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
     using C = Cfg<D, NT>;
     extern __shared__ uint8_t smem_dyn[];
     __shared__ uint32_t s_sum[kWarps];
-    __shared__ int s_b, s_rem;
+    __shared__ int s_b;
+    __shared__ uint32_t s_rem;
     const uint32_t raw = smem_u32(smem_dyn);
     uint8_t *smem = smem_dyn + ((128u - (raw & 127u)) & 127u);
     float *merge = reinterpret_cast<float *>(smem + C::kRing);
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
             rem -= n;
         }
         s_b = b;
-        s_rem = static_cast<int>(rem);
+        s_rem = rem;
     }
     __syncthreads();
 
@@ -538,9 +539,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
     // the segment's tiles, the next one for this warp
     int lb = s_b;
     Request lr = request_at<C::kRows>(p, lb);
-    int litem = static_cast<int>(static_cast<uint32_t>(s_rem) / lr.units);
+    int litem = static_cast<int>(s_rem / lr.units);
     // the segment [v, v + n) of an item's units: tiles from max(v - kItemCost, 0)
-    int lv = s_rem - litem * lr.units;
+    int lv = static_cast<int>(s_rem % lr.units);
     uint32_t ln = min(static_cast<uint32_t>(lr.units - lv), u1 - u0);
     int lt0 = max(lv - kItemCost, 0);
     uint32_t lu = u0;
@@ -615,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtasPerSm) attend_kerne
     // ---------------------------------------------------------------- segments
     int b = s_b;
     Request r = request_at<C::kRows>(p, b);
-    int item = static_cast<int>(static_cast<uint32_t>(s_rem) / r.units);
-    int v = s_rem - item * r.units;
+    int item = static_cast<int>(s_rem / r.units);
+    int v = static_cast<int>(s_rem % r.units);
     uint32_t u = u0;
     int st = 0;         // ring slot of the next tile and the parity of its use
     uint32_t ph = 0;
@@ -885,6 +886,9 @@ cudaError_t launch_one(const Params &prm, int num_sms, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, prm);
 }
 
+// 8 query rows per key/value head fill one MMA column tile, more take two
+constexpr bool narrow(int64_t rows) { return rows <= 8; }
+
 constexpr size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 constexpr int kMaxRows = 16;
 constexpr size_t kDescBytes = round256(sizeof(Desc) * kMaxCtas);
@@ -898,6 +902,12 @@ cudaError_t configure_kv4_attend()
     for (cudaError_t x : r)
         if (x != cudaSuccess) return x;
     return cudaSuccess;
+}
+
+bool kv4_attend_countable(int64_t B, int64_t heads, int64_t rows, int64_t tokens)
+{
+    const int64_t item = narrow(rows) ? 8 : kMaxRows;
+    return B * heads * ((rows + item - 1) / item) <= UINT32_MAX / ((tokens + kTile - 1) / kTile + kItemCost);
 }
 
 size_t kv4_attend_workspace(int D)
@@ -916,12 +926,11 @@ cudaError_t launch_kv4_attend(const Kv4AttendArgs &a, int64_t max_rows, void *ws
     prm.group = a.q_heads / a.cache.heads;
     prm.max_rows = max_rows;
     prm.uk = unpack_consts();
-    // 8 query rows per key/value head fill one MMA column tile, more take two
     const int64_t rows = static_cast<int64_t>(a.max_new) * prm.group;
-    const bool narrow = (rows < max_rows ? rows : max_rows) <= 8;
+    const bool one = narrow(rows < max_rows ? rows : max_rows);
     if (a.cache.D == 128)
-        return narrow ? launch_one<128, 1>(prm, num_sms, st) : launch_one<128, 2>(prm, num_sms, st);
-    return narrow ? launch_one<64, 1>(prm, num_sms, st) : launch_one<64, 2>(prm, num_sms, st);
+        return one ? launch_one<128, 1>(prm, num_sms, st) : launch_one<128, 2>(prm, num_sms, st);
+    return one ? launch_one<64, 1>(prm, num_sms, st) : launch_one<64, 2>(prm, num_sms, st);
 }
 
 }  // namespace awq
