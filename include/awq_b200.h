@@ -423,7 +423,9 @@ AWQ_API size_t awq_kv4_page_bytes(int64_t page_size, int64_t D);
  * Device errors: AWQ_ERR_RANGE (a negative length, more tokens than T, more
  * pages than max_pages, free_count outside 0..num_pages), AWQ_ERR_CAPACITY (too few
  * free pages).  Then nothing is reserved: slots and positions are -1, cu is 0,
- * lengths, table and stack are unchanged.
+ * lengths, table and stack are unchanged.  AWQ_ERR_RANGE also for a page outside
+ * the cache, in the table where new tokens go or on the stack: those tokens get slot
+ * -1, a table entry from the stack becomes -1, and the rest of the step stands.
  */
 AWQ_API awq_status_t awq_kv4_reserve(const int32_t *new_lens, const int32_t *lens, int64_t B,
                                      int64_t page_size, int32_t *block_table, int64_t max_pages,

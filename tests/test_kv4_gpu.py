@@ -649,3 +649,33 @@ def test_wide_tables_and_long_chunks():
     p, c, table = _filled(lens, Hk, D, page, seed=3, max_pages=4096)
     cu = np.concatenate([[0], np.cumsum(new)]).tolist()
     _check_attention(c, table, _rows(cu[-1], 32, D, 5), cu, lens, 2048)
+
+
+@pytest.mark.parametrize("bad", [-1, -7, 12, 2**31 - 1])
+@pytest.mark.parametrize("total_extra", [0, 5000])
+def test_reserve_reports_bad_pages_and_does_not_follow_them(bad, total_extra):
+    # a held page and a page on the stack that the cache does not have: their tokens have no slot, the others do
+    page, table, free = 16, [[4, 1, -1, -1], [6, -1, -1, -1], [3, -1, -1, -1]], [0, 2, 5, 7]
+    lens, add = [17, 9, 16], [20, 3, 18]       # request 0 goes on in page 1 and takes 7; 2 takes 5 and 2
+    total = sum(add) + total_extra
+    for where in ("none", "held", "free"):
+        t, f = np.array(table, np.int32), np.array(free + [-1] * 8, np.int32)
+        if where == "held":
+            t[1, 0] = bad
+        if where == "free":
+            f[2] = bad
+        want = list(ref.reserve(add, lens, t, f, 4, page, total))
+        if where == "held":
+            want[0][20:23] = -1
+        if where == "free":
+            want[0][23:39] = -1
+            want[5][2, 1] = -1
+        p = awq.KV4Pages(12, page, 3, 4, block_table=torch.from_numpy(t).cuda(), free_pages=torch.from_numpy(f).cuda(),
+                         lens=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                         free_count=torch.tensor([4], dtype=torch.int32, device="cuda"))
+        st = awq.new_status("cuda")
+        slots, pos, cu = p.reserve(torch.tensor(add, dtype=torch.int32, device="cuda"), total, status=st)
+        assert int(st) == (awq.OK if where == "none" else awq.ERR_RANGE)
+        for g, w, name in zip((slots, pos, cu, p.lens, p.free_count, p.block_table), want,
+                              ("slots", "positions", "cu", "lens", "free_count", "table")):
+            assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), (where, name)

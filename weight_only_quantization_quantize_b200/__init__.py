@@ -687,7 +687,8 @@ class KV4Pages:
         Returns (slots int64 [total], positions int32 [total], cu int32 [max_requests + 1]); slots and positions are
         -1 in the padding.  The new lengths and free count go to next_lens and next_free (default: in place).
         status receives ERR_CAPACITY when the free pages do not suffice, ERR_RANGE for impossible lengths; then nothing
-        is reserved and every slot is -1."""
+        is reserved and every slot is -1.  ERR_RANGE also for a page outside the cache, held or free: its tokens get
+        slot -1, the others their slots."""
         dev, B = self.device, self.max_requests
         _match(new_lens, torch.int32, (B,), "new_lens", dev)
         if not 1 <= total < 2**31:

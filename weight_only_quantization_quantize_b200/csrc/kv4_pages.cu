@@ -160,6 +160,12 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveParams p
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) page[i] = entry[i] ? *entry[i] : -1;
 #pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (entry[i] && (page[i] < 0 || page[i] >= p.num_pages)) {  // its tokens have no slot
+                page[i] = -1;
+                report(p.status, AWQ_ERR_RANGE);
+            }
+#pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int64_t t = t0 + i * stride;
             if (t >= p.T) break;
@@ -172,7 +178,9 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveParams p
     for (int64_t i = tid; i < pages; i += stride) {
         const int b = owner_of(s_first, p.B, static_cast<int>(i));
         const int held = (s_len[b] + P1) >> p.page_shift;
-        p.block_table[static_cast<size_t>(b) * p.max_pages + held + (i - s_first[b])] = p.free_pages[free0 - 1 - i];
+        const int page = p.free_pages[free0 - 1 - i];  // a bad one has been reported with its tokens
+        p.block_table[static_cast<size_t>(b) * p.max_pages + held + (i - s_first[b])] =
+            page < 0 || page >= p.num_pages ? -1 : page;
     }
     // every CTA has read the lengths and the free count: they may be replaced
     cluster_arrive_release();
