@@ -439,10 +439,12 @@ AWQ_API awq_status_t awq_kv4_reserve(const int32_t *new_lens, const int32_t *len
  * the stack, in the order of requests, then of positions; its length becomes 0
  * and the table entries of those pages -1.
  *   done int32 [B]; lens, block_table, free_pages, free_count updated in place
+ * Entries of -1 are passed over: pages before a sliding window that the caller has
+ * already pushed (to free_pages[free_count], entry -1, free_count + 1).
  * Device errors: AWQ_ERR_RANGE (a length or page out of range, more pages than
- * num_pages in the stack); then nothing is changed.  Every page of an ended
- * request has to be in its row, and in no other request's: a page that two rows
- * share would be pushed twice, which is not detected.
+ * num_pages in the stack); then nothing is changed.  Every page that an ended
+ * request still holds has to be in its row, and in no other request's: a page
+ * that two rows share would be pushed twice, which is not detected.
  */
 AWQ_API awq_status_t awq_kv4_release(const int32_t *done, int32_t *lens, int64_t B, int64_t page_size,
                                      int32_t *block_table, int64_t max_pages, int32_t *free_pages,

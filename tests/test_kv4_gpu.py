@@ -679,3 +679,95 @@ def test_reserve_reports_bad_pages_and_does_not_follow_them(bad, total_extra):
         for g, w, name in zip((slots, pos, cu, p.lens, p.free_count, p.block_table), want,
                               ("slots", "positions", "cu", "lens", "free_count", "table")):
             assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), (where, name)
+
+
+@pytest.mark.parametrize("B,page,most", [(1, 16, 40), (5, 32, 700), (300, 16, 90), (4096, 16, 3), (7, 256, 5000)])
+def test_release_passes_over_pages_that_are_gone(B, page, most):
+    # rows that have given back pages before their window, and rows that have not, in one call
+    r = random.Random(B)
+    held = [r.randint(0, most) for _ in range(B)]
+    lens = [h * page - r.randint(0, page - 1) if h else 0 for h in held]
+    gone = [r.choice([0, r.randint(0, h), max(h - 1, 0)]) for h in held]
+    done = [int(r.random() < 0.6) for _ in range(B)]
+    done[0] = 1
+    num = sum(held) + 4
+    order = list(range(num))
+    r.shuffle(order)
+    table = np.full((B, most + 1), -1, np.int32)
+    free = order[sum(held):]
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = order[at: at + h]
+        free += table[b, : gone[b]].tolist()       # given back by their holder
+        table[b, : gone[b]] = -1
+        at += h
+    if held[0] > gone[0] + 2:                      # and one out of the middle
+        free.append(int(table[0, gone[0] + 1]))
+        table[0, gone[0] + 1] = -1
+    p = awq.KV4Pages(num, page, B, most + 1, block_table=torch.from_numpy(table).cuda(),
+                     lens=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                     free_pages=torch.tensor(free + [-1] * (num - len(free)), dtype=torch.int32, device="cuda"),
+                     free_count=torch.tensor([len(free)], dtype=torch.int32, device="cuda"))
+    st = awq.new_status("cuda")
+    p.release(torch.tensor(done, dtype=torch.int32, device="cuda"), status=st)
+    awq.raise_on_status(st)
+    back = [int(x) for b in range(B) if done[b] for x in table[b, : held[b]] if x >= 0]
+    count = len(free) + len(back)
+    assert int(p.free_count) == count
+    assert p.free_pages[:count].tolist() == free + back
+    assert p.lens.tolist() == [0 if d else n for d, n in zip(done, lens)]
+    for b in range(B):
+        if done[b]:
+            table[b, : held[b]] = -1
+    assert np.array_equal(p.block_table.cpu().numpy(), table)
+
+
+def test_a_request_under_a_window_gives_its_pages_back_and_ends():
+    # as a server runs it: tokens appended and attended to under a window, pages before it given back as they leave it
+    page, window, D = 16, 40, 64
+    p = awq.KV4Pages(8, page, 1, 40)               # 8 pages for a request of 33 pages: only with the window
+    c = awq.KV4Cache(p, 1, D)
+    st, gone, host = awq.new_status("cuda"), 0, np.zeros((40, 1, awq.kv4_page_bytes(page, D)), np.uint8)
+    for i, m in enumerate([30] + [7] * 70):
+        slots, pos, cu = p.reserve(torch.tensor([m], dtype=torch.int32, device="cuda"), m, status=st)
+        k, v, q = _rows(m, 1, D, 3 * i), _rows(m, 1, D, 3 * i + 1), _rows(m, 2, D, 3 * i + 2)
+        c.append(k.cuda(), v.cuda(), slots, status=st)
+        out = c.attention(q.cuda(), cu=cu, max_new=m, window=window, status=st)
+        awq.raise_on_status(st)
+        ref.store(host, k.numpy(), v.numpy(), pos.tolist(), page)
+        n = int(p.lens)
+        if i % 10 == 0:
+            want, bound = ref.attention(q, host, np.arange(40)[None], [n], [0, m], page, D ** -0.5, window)
+            assert bool(((out.cpu().double() - want).abs() <= bound).all())
+        while (gone + 1) * page <= n - window + 1:  # the next query stands at n and sees n - window + 1 on
+            p.free_pages[p.free_count.long()] = p.block_table[0, gone]
+            p.block_table[0, gone] = -1
+            p.free_count += 1
+            gone += 1
+    assert gone > 20
+    p.release(torch.ones(1, dtype=torch.int32, device="cuda"), status=st)
+    awq.raise_on_status(st)
+    assert int(p.free_count) == 8 and sorted(p.free_pages.tolist()) == list(range(8)) and int(p.lens) == 0
+    assert bool((p.block_table == -1).all())
+
+
+@pytest.mark.parametrize("bad", [-2, 6, 2**31 - 1, -2**31])
+def test_release_refuses_pages_outside_the_cache(bad):
+    table = torch.tensor([[4, -1, bad, 2], [1, 3, -1, -1]], dtype=torch.int32, device="cuda")
+    p = awq.KV4Pages(6, 16, 2, 4, block_table=table, lens=torch.tensor([60, 20], dtype=torch.int32, device="cuda"),
+                     free_pages=torch.tensor([0, 5, -1, -1, -1, -1], dtype=torch.int32, device="cuda"),
+                     free_count=torch.tensor([2], dtype=torch.int32, device="cuda"))
+    state = (p.block_table, p.lens, p.free_pages, p.free_count)
+    before = [t.clone() for t in state]
+    st = awq.new_status("cuda")
+    p.release(torch.ones(2, dtype=torch.int32, device="cuda"), status=st)
+    assert int(st) == awq.ERR_RANGE and all(torch.equal(a, b) for a, b in zip(before, state))
+    st = awq.new_status("cuda")
+    p.free_count.fill_(5)          # two pages would make seven of six
+    p.release(torch.tensor([0, 1], dtype=torch.int32, device="cuda"), status=st)
+    assert int(st) == awq.ERR_RANGE and p.lens.tolist() == [60, 20] and int(p.free_count) == 5
+    st = awq.new_status("cuda")
+    p.free_count.fill_(2)
+    p.release(torch.tensor([0, 1], dtype=torch.int32, device="cuda"), status=st)
+    awq.raise_on_status(st)
+    assert p.free_pages.tolist()[:4] == [0, 5, 1, 3] and int(p.free_count) == 4

@@ -719,7 +719,9 @@ class KV4Pages:
     def release(self, done, status=None):
         """Ends the requests with done[b] != 0 (int32 [max_requests]): their pages return to the stack.
 
-        Every page of such a request must be in its row of the table and in no other request's."""
+        Every page that such a request holds must be in its row of the table and in no other request's.  Entries of -1
+        are passed over: pages before a sliding window may be given back earlier, by writing them to
+        free_pages[free_count], raising free_count and setting their entries to -1."""
         dev = self.device
         _match(done, torch.int32, (self.max_requests,), "done", dev)
         if status is not None:
