@@ -135,10 +135,15 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, ui
     const cuuint64_t strides[1] = {row_bytes};
     const cuuint32_t box[2] = {box_inner, box_outer};
     const cuuint32_t elem[2] = {1, 1};
-    if (g_encode(map, dtype, 2, const_cast<void *>(base), dims, strides, box, elem,
-                 CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    auto encode = [&] {
+        return g_encode(map, dtype, 2, const_cast<void *>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = encode();
+    // The encoder is a driver call and wants a current context, which a host thread
+    // has only after its first runtime call that needs one.
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(dev) == cudaSuccess) r = encode();
+    if (r != CUDA_SUCCESS) return false;
     int slot;
     if (c.used < kMapCache) {
         slot = c.used++;
