@@ -231,7 +231,9 @@ AWQ_API awq_status_t awq_quantize_pack_clip(const uint16_t *W, const uint16_t *s
  * X / s and, for M >= 64, the partial sums of output tiles whose k range is
  * split between CTAs (at most 20 MB); it is overwritten.  The size depends on
  * M, K and N, not on the device.  Calls on one stream may share a
- * workspace; calls that can run at the same time need separate ones.  After a
+ * workspace, as long as no two host threads make them at once: a call enqueues
+ * up to two kernels that pass X / s through it, and the other call's must not
+ * come between.  Calls that can run at the same time need separate ones.  After a
  * device error (AWQ_ERR_DEVICE_TIMEOUT) zero the workspace again.
  * Device errors: AWQ_ERR_DEVICE_TIMEOUT if an internal pipeline wait ran out
  * (Y is then unspecified).  For M >= 64 with few output tiles the call may run
@@ -346,7 +348,8 @@ AWQ_API awq_status_t awq_scale_search(const uint16_t *xcal, int64_t R, int64_t K
  * without a device error leaves it at zero; the rest is written before it is
  * read.  Calls whose executions overlap on the GPU (different streams without
  * ordering between them) race on the scratch array and give undefined
- * results; order them on one stream or with events.
+ * results; order them on one stream or with events.  Host threads may make
+ * calls on one stream at the same time: each call's kernels are enqueued together.
  */
 #define AWQ_NOALLOC_SCRATCH_BYTES ((size_t)24 << 20)
 AWQ_API awq_status_t awq_w4a16_gemm_noalloc(const uint16_t *X, const uint16_t *s, const int32_t *Q,
@@ -499,7 +502,8 @@ AWQ_API awq_status_t awq_kv4_load(const int64_t *slots, int64_t T, int64_t kv_he
  *   out     binary16 [T, q_heads, D] (output); rows of no request are not written
  *   workspace  at least awq_kv4_attention_workspace_size(D) bytes, no initial
  *           contents required, overwritten; calls that can run at the same time
- *           need separate ones
+ *           need separate ones, and so do calls of two host threads, on one
+ *           stream too (a call enqueues up to four kernels that share it)
  *   q_heads % kv_heads == 0, both <= AWQ_KV4_MAX_HEADS; 1 <= B <=
  *   AWQ_KV4_MAX_REQUESTS; 1 <= T, max_new < 2^31; tokens = max_pages * page_size < 2^31;
  *   with rows = max_new * q_heads / kv_heads (requests of more than 48 rows go to the

@@ -38,6 +38,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 
 import torch
 
@@ -339,6 +340,21 @@ def gemm_workspace_size(M: int, K: int, N: int) -> int:
 # share one workspace; calls on different streams get different ones.
 _workspaces: dict = {}
 
+# A call enqueues up to four kernels that pass data through its workspace, and
+# ctypes lets other threads run meanwhile: the calls that use a stream's default
+# workspaces take that stream's lock, so that their kernels stay together.
+# (Re-entrant: an allocation inside may run a finalizer that calls the library.)
+_stream_locks: dict = {}
+_NO_LOCK = contextlib.nullcontext()
+
+
+def _stream_lock(index: int, stream: int, workspace):
+    """What a call holds while it enqueues; nothing for a workspace that the caller has brought."""
+    if workspace is not None:
+        return _NO_LOCK
+    lock = _stream_locks.get((index, stream))
+    return lock if lock is not None else _stream_locks.setdefault((index, stream), threading.RLock())
+
 
 def workspace_for(device: torch.device, nbytes: int) -> torch.Tensor:
     """The zero-filled workspace this binding uses on `device`'s current stream,
@@ -427,8 +443,9 @@ def w4a16_gemm(X, s, Q, scales, zeros, status=None, out=None, workspace=None) ->
     """Y = (X / s) . dequant(Q), float16 [M, N].
 
     workspace: a uint8 CUDA tensor of at least gemm_workspace_size(M, K, N)
-    bytes, zero-filled before its first use (the calls keep it that way); by
-    default a cached zero-filled workspace of the current stream is used."""
+    bytes, zero-filled before its first use (the calls keep it that way), not
+    used by two threads at once; by default a cached zero-filled workspace of
+    the current stream is used."""
     _need(X, torch.float16, 2, "X")
     M, K = X.shape
     dev = X.device
@@ -442,7 +459,7 @@ def w4a16_gemm(X, s, Q, scales, zeros, status=None, out=None, workspace=None) ->
     else:
         _check_out(out, M, N, dev)
         Y = out
-    with _on(dev):
+    with _on(dev), _stream_lock(dev.index, _raw_stream(dev), workspace):
         wsz = gemm_workspace_size(M, K, N)
         if workspace is None:
             workspace = workspace_for(dev, wsz)
@@ -474,7 +491,7 @@ def w4a16_gemv(X, s, Q, scales, zeros, status=None, out=None, workspace=None) ->
     else:
         _check_out(out, 1, N, dev)
         Y = out
-    with _on(dev):
+    with _on(dev), _stream_lock(dev.index, _raw_stream(dev), workspace):
         wsz = int(lib().awq_w4a16_gemv_workspace_size(K, N))
         if workspace is None:
             workspace = workspace_for(dev, wsz)
@@ -533,7 +550,7 @@ def w4a16_gemm_epilogue(X, s, Q, scales, zeros, bias=None, act=None, gated=False
     else:
         _check_out(out, M, cols, dev)
         Y = out
-    with _on(dev):
+    with _on(dev), _stream_lock(dev.index, _raw_stream(dev), workspace):
         wsz = gemm_workspace_size(M, K, N)
         if workspace is None:
             workspace = _epilogue_workspace(dev, wsz)
@@ -599,22 +616,21 @@ class QuantLinear:
         stream = torch._C._cuda_getCurrentRawStream(self._dev_index)
         wsz = self._lib.awq_w4a16_gemm_workspace_size(M, self.K, self.N)
         plain = self._plain and residual is None
-        if workspace is not None:
-            _check_workspace(workspace, wsz, self.device)
-        elif plain:
-            workspace = workspace_for(self.device, wsz)
-        else:
-            workspace = _epilogue_workspace(self.device, wsz)
         s, q, sc, z = self._wptrs
-        if not plain:
-            _call(self.device, "awq_w4a16_gemm_epilogue", self._lib.awq_w4a16_gemm_epilogue, X.data_ptr(), s, q, sc, z,
-                  M, self.K, self.N, self._bptr, self._act, self._gate, _ptr(residual), out.data_ptr(),
-                  workspace.data_ptr(), workspace.numel(), _ptr(status), stream)
-            return out
-        with _on(self.device):
-            _check(self._lib.awq_w4a16_gemm(X.data_ptr(), s, q, sc, z, M, self.K, self.N, out.data_ptr(),
-                                            workspace.data_ptr(), workspace.numel(), _ptr(status), stream),
-                   "awq_w4a16_gemm")
+        with _stream_lock(self._dev_index, stream, workspace):
+            if workspace is not None:
+                _check_workspace(workspace, wsz, self.device)
+            elif plain:
+                workspace = workspace_for(self.device, wsz)
+            else:
+                workspace = _epilogue_workspace(self.device, wsz)
+            if not plain:
+                _call(self.device, "awq_w4a16_gemm_epilogue", self._lib.awq_w4a16_gemm_epilogue, X.data_ptr(), s, q, sc,
+                      z, M, self.K, self.N, self._bptr, self._act, self._gate, _ptr(residual), out.data_ptr(),
+                      workspace.data_ptr(), workspace.numel(), _ptr(status), stream)
+            else:
+                _call(self.device, "awq_w4a16_gemm", self._lib.awq_w4a16_gemm, X.data_ptr(), s, q, sc, z, M, self.K,
+                      self.N, out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status), stream)
         return out
 
 
@@ -822,8 +838,8 @@ class KV4Cache:
         Returns [T, q_heads, head_dim]; rows of no request are not written.
         AwqError (ERR_SHAPE) for bounds whose work is not counted in 32 bits: max_requests * kv_heads *
         (1 to 3, by rows of a request) * (max_pages * page_size / 64 + 8) has to stay below 2**32.
-        workspace: uint8 of kv4_attention_workspace_size(head_dim) bytes; by default the stream's cached one, or the
-        graph's own during capture."""
+        workspace: uint8 of kv4_attention_workspace_size(head_dim) bytes, not used by two threads at once; by default
+        the stream's cached one, or the graph's own during capture."""
         p = self.pages
         dev, D = p.device, self.head_dim
         if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != D or q.dtype is not torch.float16 \
@@ -850,15 +866,16 @@ class KV4Cache:
         if T == 0:
             return out
         stream = _raw_stream(dev)
-        if workspace is not None:
-            _check_workspace(workspace, self._workspace_size, dev)
-        elif _capturing():
-            workspace = torch.empty(self._workspace_size, dtype=torch.uint8, device=dev)
-        else:
-            workspace = _kv4_workspace(dev, stream, self._workspace_size)
-        _call(dev, "awq_kv4_attention", self._lib.awq_kv4_attention, q.data_ptr(), st[0] if T > 1 else H * D, T, H,
-              *self._read, _ptr(cu), p.max_requests, max_new, D ** -0.5 if scale is None else scale, window,
-              out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status), stream)
+        with _stream_lock(dev.index, stream, workspace):
+            if workspace is not None:
+                _check_workspace(workspace, self._workspace_size, dev)
+            elif _capturing():
+                workspace = torch.empty(self._workspace_size, dtype=torch.uint8, device=dev)
+            else:
+                workspace = _kv4_workspace(dev, stream, self._workspace_size)
+            _call(dev, "awq_kv4_attention", self._lib.awq_kv4_attention, q.data_ptr(), st[0] if T > 1 else H * D, T, H,
+                  *self._read, _ptr(cu), p.max_requests, max_new, D ** -0.5 if scale is None else scale, window,
+                  out.data_ptr(), workspace.data_ptr(), workspace.numel(), _ptr(status), stream)
         return out
 
 

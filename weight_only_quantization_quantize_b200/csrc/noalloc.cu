@@ -19,9 +19,12 @@ static __device__ __align__(256) uint8_t g_noalloc_scratch[AWQ_NOALLOC_SCRATCH_B
 constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mutex;
 void *g_scratch_addr[kMaxDevices] = {};
+// A call enqueues up to two kernels that share the scratch array: held meanwhile,
+// so that those of another host thread's call on the stream do not come between.
+std::mutex g_call_mutex[kMaxDevices];
 
 // Device address of this device's scratch array (looked up on first use).
-awq_status_t scratch_for_current_device(void **addr)
+awq_status_t scratch_for_current_device(void **addr, int *device)
 {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -39,6 +42,7 @@ awq_status_t scratch_for_current_device(void **addr)
         g_scratch_addr[dev] = p;
     }
     *addr = g_scratch_addr[dev];
+    *device = dev;
     return AWQ_OK;
 }
 
@@ -56,8 +60,10 @@ extern "C" awq_status_t awq_w4a16_gemm_noalloc(const uint16_t *X, const uint16_t
     if (e != AWQ_OK) return e;
     if (awq_w4a16_gemm_workspace_size(M, K, N) > AWQ_NOALLOC_SCRATCH_BYTES) return AWQ_ERR_WORKSPACE;
     void *scratch = nullptr;
-    e = scratch_for_current_device(&scratch);
+    int dev = 0;
+    e = scratch_for_current_device(&scratch, &dev);
     if (e != AWQ_OK) return e;
+    std::lock_guard<std::mutex> lock(g_call_mutex[dev]);
     return awq::matmul_with_workspace(X, s, Q, scales, zeros, M, K, N, Y, scratch,
                                       AWQ_NOALLOC_SCRATCH_BYTES, dev_status, stream);
 }
