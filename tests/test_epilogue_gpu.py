@@ -184,3 +184,35 @@ def test_chained_residuals():
                 w, bound = _finish(t, e, None, None, False, x)
                 assert bool(((nxt.double() - w).abs() <= bound).all())
                 x = nxt
+
+
+@pytest.mark.parametrize("M", [1, 3, 16, 40, 100, 300])
+@pytest.mark.parametrize("entry", ["layer", "gemm"])
+def test_captured_plain_products_replayed_together(M, entry):
+    # as above without an epilogue: graphs captured on one fresh stream, the second one replayed first and both at
+    # the same time, then eager calls on that stream
+    K, N = 2048, 512
+    side, made = torch.cuda.Stream(), []
+    for n in range(2):
+        X, s, Q, sc, z = _layer(M, K, N, 30 + n, scaled=True)
+        lin = awq.QuantLinear(Q, sc, z, s)
+        call = (lambda X, out, lin=lin: lin(X, out=out)) if entry == "layer" else \
+            (lambda X, out, a=(s, Q, sc, z): awq.w4a16_gemm(X, *a, out=out))
+        want = torch.empty(M, N, dtype=torch.float16, device="cuda")
+        call(X, want)
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            call(X, out)
+        made.append((g, want, out, call, X, lin))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(20):
+        for (g, *_), st in zip(made[::-1], streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    with torch.cuda.stream(side):
+        eager = [call(X, torch.empty_like(want)) for _, want, _, call, X, _ in made]
+    torch.cuda.synchronize()
+    for (g, want, out, *_), e in zip(made, eager):
+        assert torch.equal(out, want) and torch.equal(e, want)

@@ -367,6 +367,19 @@ def workspace_for(device: torch.device, nbytes: int) -> torch.Tensor:
     return ws
 
 
+def _default_workspace(dev: torch.device, M: int, need: int) -> torch.Tensor:
+    """Default workspace of a product of M tokens: the stream's cached one.  A call that is being captured into
+    a graph gets its own, from the graph's memory: graphs captured on one stream may be replayed at the same
+    time on others, and a cached one's zeroes would be written by the first graph's replays only.  From
+    64 tokens on, where the counters are used, the graph zeroes them."""
+    if not _capturing():
+        return workspace_for(dev, need)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    if M >= 64:
+        ws[:32768].zero_()
+    return ws
+
+
 def scales_alpha(m: torch.Tensor, j: int, status: torch.Tensor | None = None) -> torch.Tensor:
     """Scales of grid point alpha = j/8: s = m^(j/8) normalised, float16 [K]."""
     _need(m, torch.float32, 1, "m")
@@ -445,7 +458,7 @@ def w4a16_gemm(X, s, Q, scales, zeros, status=None, out=None, workspace=None) ->
     workspace: a uint8 CUDA tensor of at least gemm_workspace_size(M, K, N)
     bytes, zero-filled before its first use (the calls keep it that way), not
     used by two threads at once; by default a cached zero-filled workspace of
-    the current stream is used."""
+    the current stream is used, or the graph's own during capture."""
     _need(X, torch.float16, 2, "X")
     M, K = X.shape
     dev = X.device
@@ -462,7 +475,7 @@ def w4a16_gemm(X, s, Q, scales, zeros, status=None, out=None, workspace=None) ->
     with _on(dev), _stream_lock(dev.index, _raw_stream(dev), workspace):
         wsz = gemm_workspace_size(M, K, N)
         if workspace is None:
-            workspace = workspace_for(dev, wsz)
+            workspace = _default_workspace(dev, M, wsz)
         else:
             _check_workspace(workspace, wsz, dev)
         _check(lib().awq_w4a16_gemm(_ptr(X), _ptr(s), _ptr(Q), _ptr(scales), _ptr(zeros), M, K, N,
@@ -494,7 +507,7 @@ def w4a16_gemv(X, s, Q, scales, zeros, status=None, out=None, workspace=None) ->
     with _on(dev), _stream_lock(dev.index, _raw_stream(dev), workspace):
         wsz = int(lib().awq_w4a16_gemv_workspace_size(K, N))
         if workspace is None:
-            workspace = workspace_for(dev, wsz)
+            workspace = _default_workspace(dev, 1, wsz)
         else:
             _check_workspace(workspace, wsz, dev)
         _check(lib().awq_w4a16_gemv(_ptr(X), _ptr(s), _ptr(Q), _ptr(scales), _ptr(zeros), K, N,
@@ -512,17 +525,6 @@ def _check_epilogue(N, bias, act, gated, dev):
     if gated and N % 16:
         raise ValueError(f"a gated product needs N = {N} to be a multiple of 16")
     return ACTIVATIONS[act], int(bool(gated)), N // 2 if gated else N
-
-
-def _epilogue_workspace(dev, need):
-    """Default workspace of a call: the stream's cached one.  A call that is being captured into a graph gets its
-    own (from the graph's memory, its counters zeroed by the graph), because graphs captured on one stream
-    may be replayed at the same time on others."""
-    if _capturing():
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws[:32768].zero_()
-        return ws
-    return workspace_for(dev, need)
 
 
 def w4a16_gemm_epilogue(X, s, Q, scales, zeros, bias=None, act=None, gated=False, residual=None, status=None,
@@ -553,7 +555,7 @@ def w4a16_gemm_epilogue(X, s, Q, scales, zeros, bias=None, act=None, gated=False
     with _on(dev), _stream_lock(dev.index, _raw_stream(dev), workspace):
         wsz = gemm_workspace_size(M, K, N)
         if workspace is None:
-            workspace = _epilogue_workspace(dev, wsz)
+            workspace = _default_workspace(dev, M, wsz)
         else:
             _check_workspace(workspace, wsz, dev)
         _check(lib().awq_w4a16_gemm_epilogue(_ptr(X), _ptr(s), _ptr(Q), _ptr(scales), _ptr(zeros), M, K, N,
@@ -620,10 +622,8 @@ class QuantLinear:
         with _stream_lock(self._dev_index, stream, workspace):
             if workspace is not None:
                 _check_workspace(workspace, wsz, self.device)
-            elif plain:
-                workspace = workspace_for(self.device, wsz)
             else:
-                workspace = _epilogue_workspace(self.device, wsz)
+                workspace = _default_workspace(self.device, M, wsz)
             if not plain:
                 _call(self.device, "awq_w4a16_gemm_epilogue", self._lib.awq_w4a16_gemm_epilogue, X.data_ptr(), s, q, sc,
                       z, M, self.K, self.N, self._bptr, self._act, self._gate, _ptr(residual), out.data_ptr(),
