@@ -216,3 +216,11 @@ def test_captured_plain_products_replayed_together(M, entry):
     torch.cuda.synchronize()
     for (g, want, out, *_), e in zip(made, eager):
         assert torch.equal(out, want) and torch.equal(e, want)
+
+
+@pytest.mark.parametrize("M,K,N", [(8, 71680, 520), (23, 16640, 24584), (4, 71680, 136)])
+@pytest.mark.parametrize("bias,act,gated,residual", [(True, "gelu", False, True), (False, "silu", True, False), (False, None, True, True)])
+def test_long_reductions_of_the_register_fed_path(M, K, N, bias, act, gated, residual):
+    # more than 64 groups per CTA: steps and zero points are read from global memory
+    test_every_path_and_epilogue(M, K, N, bias, act, gated, residual)
+    test_an_empty_epilogue_is_the_plain_product(M, K, N)

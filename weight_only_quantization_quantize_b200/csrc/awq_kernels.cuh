@@ -39,7 +39,7 @@ cudaError_t launch_gemv(const GemvPlan &plan, const CUtensorMap &tmQ, const __ha
                         int M, int K, int N, int32_t *status, const Epilogue *epi,
                        cudaStream_t st);
 
-// matmul_small.cu -- M < 64: register-fed tensor cores, TMA weight stream
+// matmul_small.cu -- M < 24: register-fed tensor cores, TMA weight stream
 struct SmallMPlan {
     int mt;          // token tiles of 8
     bool prologue;   // X / s computed inside the kernel (no workspace)

@@ -1,4 +1,4 @@
-// matmul_small.cu -- Y = (X / s) . dequant(Q) for M < 64 tokens (decode and
+// matmul_small.cu -- Y = (X / s) . dequant(Q) for M < 24 tokens (decode and
 // small batches), the HBM-bound regime of the W4A16 linear layer.
 //
 // Sources: lansai AWQ explainer (ai.lansai.wang/107648), "AWQ 的四步链路"
@@ -7,7 +7,7 @@
 // "Group Size Configuration" / "Zero-Point Quantization" (4-bit codes, group
 // 128, zero point).
 //
-// Design (B200), for 1 <= M < 64 tokens (the single-token GEMV with small K
+// Design (B200), for 1 <= M < 24 tokens (the single-token GEMV with small K
 // uses gemv.cu instead):
 //  * Weights stream once from HBM: a producer warp issues TMA tile loads of
 //    the packed words (one 16-row x 32-column box per consumer warp, 128-byte
@@ -20,7 +20,7 @@
 //    (two LOP3 masks + f16x2 ops per pair, the step applied in binary16 as in
 //    the tensor-core GEMM) and feeds them from registers to mma.sync m16n8k16
 //    (fp32 accumulate) in swap-AB form: output columns are the MMA rows, the
-//    M tokens (up to 8 tiles of 8) its columns.  The contraction order inside
+//    M tokens (up to 3 tiles of 8) its columns.  The contraction order inside
 //    each 8-k word is permuted (pairs (0,4),(1,5),(2,6),(3,7)); X / s is stored
 //    with the same permutation.
 //  * Split-K across the CTAs of a thread-block cluster; each CTA pushes its
@@ -433,10 +433,8 @@ int stage_bytes_for(int M)
 
 cudaError_t configure_small_m()
 {
-    const cudaError_t r[] = {configure_one<1, 4>(), configure_one<2, 4>(), configure_one<3, 4>(), configure_one<4, 4>(),
-                             configure_one<5, 4>(), configure_one<6, 4>(), configure_one<7, 4>(),
-                             configure_one<8, 4>(), configure_one<1, 3>(), configure_one<2, 3>(),
-                             configure_one<3, 3>()};
+    const cudaError_t r[] = {configure_one<1, 4>(), configure_one<2, 4>(), configure_one<3, 4>(),
+                             configure_one<1, 3>(), configure_one<2, 3>(), configure_one<3, 3>()};
     for (cudaError_t x : r)
         if (x != cudaSuccess) return x;
     return cudaSuccess;
@@ -450,7 +448,7 @@ SmallMPlan plan_small_m(int M, int K, int N, int num_sms)
     pl.n_tiles = (N + kBN - 1) / kBN;
     pl.prologue = false;
     pl.kh = 1;
-    // A 4-deep ring, or 3-deep (up to 24 tokens) when that lets more CTAs
+    // A 4-deep ring, or 3-deep when that lets more CTAs
     // share an SM and so a finer split fit in one wave: measured on the 13B
     // set, resident CTAs beat ring depth (8 deep lost 8% at 8 tokens and 30%
     // at 16 against 4 deep).
@@ -460,7 +458,7 @@ SmallMPlan plan_small_m(int M, int K, int N, int num_sms)
     const int stage_bytes = stage_bytes_for(M);
     const int recv_bytes = 8 * pl.mt * kBN * 4;
     int best_splits = 0;
-    for (int stages = 4; stages >= (pl.mt <= 3 ? 3 : 4); --stages) {
+    for (int stages = 4; stages >= 3; --stages) {
         // one wave: the largest power-of-two split with n_tiles * splits <= CTAs
         // resident (the steps and zero words of a CTA's groups shrink as the
         // split grows)
@@ -540,11 +538,6 @@ cudaError_t launch_small_m(const SmallMPlan &plan, const CUtensorMap &tmQ, const
     case 1: return launch_either<1, 4>(plan, tmQ, tmX, prm, e, st);
     case 2: return launch_either<2, 4>(plan, tmQ, tmX, prm, e, st);
     case 3: return launch_either<3, 4>(plan, tmQ, tmX, prm, e, st);
-    case 4: return launch_either<4, 4>(plan, tmQ, tmX, prm, e, st);
-    case 5: return launch_either<5, 4>(plan, tmQ, tmX, prm, e, st);
-    case 6: return launch_either<6, 4>(plan, tmQ, tmX, prm, e, st);
-    case 7: return launch_either<7, 4>(plan, tmQ, tmX, prm, e, st);
-    case 8: return launch_either<8, 4>(plan, tmQ, tmX, prm, e, st);
     default: return cudaErrorInvalidValue;
     }
 }
