@@ -74,3 +74,22 @@ def test_scale_search_waits_run_out_and_the_context_survives(waitlib):  # noqa: 
     assert int(st) == awq.ERR_TIMEOUT
     for a, b in zip(awq.scale_search(x, W), before):
         assert torch.equal(a, b)
+
+
+def test_quantizer_waits_run_out_and_the_context_survives(waitlib):  # noqa: F811
+    f = waitlib.awq_quantize_pack
+    f.argtypes = [P, P, I64, I64, P, P, P, P, P]
+    f.restype = ctypes.c_int
+    K, N = 4096, 6144
+    g = torch.Generator(device="cuda").manual_seed(2)
+    W, s = torch.randn(K, N, generator=g, device="cuda").half(), torch.ones(K, dtype=torch.float16, device="cuda")
+    before = awq.quantize_pack(W, s)
+    for _ in range(3):
+        Q, sc, z = (torch.zeros_like(t) for t in before)
+        st = awq.new_status("cuda")
+        torch.cuda.synchronize()
+        assert f(_p(W), _p(s), K, N, _p(Q), _p(sc), _p(z), _p(st), torch.cuda.current_stream().cuda_stream) == awq.OK
+        torch.cuda.synchronize()
+        code = int(st)      # garbage read too early may also look like a value that is not finite
+        assert code in (awq.ERR_TIMEOUT, awq.ERR_NONFINITE) or (code == awq.OK and torch.equal(Q, before[0]))
+        assert all(torch.equal(a, b) for a, b in zip(awq.quantize_pack(W, s), before))

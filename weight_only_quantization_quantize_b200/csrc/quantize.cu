@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(kQThreads, 1) quantize_pack_kernel(const __gri
     // this half's tiles: first, then every (2 * gridDim.x)-th
     const int t_first = 2 * blockIdx.x + half;
     const int t_step = 2 * gridDim.x;
+    int issued = 0;  // by thread 0 of the half, stages in turn
     auto issue = [&](int t, int st) {
+        ++issued;
         const int g = t / p.n_ctiles;
         const int ct = t - g * p.n_ctiles;
         mbar_arrive_expect_tx(&sm.full[st], kQTileBytes);
@@ -356,7 +358,8 @@ __global__ void __launch_bounds__(kQThreads, 1) quantize_pack_kernel(const __gri
         named_bar_sync(bar_id, 256);  // the stage is read, the partial extremes are written
 
         // the stage is free: bring this half's tile two steps ahead
-        if (tid == 0 && t + 2 * t_step < p.tiles) issue(t + 2 * t_step, st);
+        // (not after a wait that ran out: the slot's barrier may still expect its last copy)
+        if (tid == 0 && ok && t + 2 * t_step < p.tiles) issue(t + 2 * t_step, st);
 
         // ---- one thread per column: step, zero point, reciprocal, clamp flag
         if (tid < kQTileN) {
@@ -485,6 +488,10 @@ __global__ void __launch_bounds__(kQThreads, 1) quantize_pack_kernel(const __gri
     }
     if (bad) report(p.status, AWQ_ERR_NONFINITE);
     if (!ok && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+    // the copies issued land before the CTA exits, whichever thread's wait ran out
+    if (tid == 0)
+        for (int i = issued > 2 ? issued - 2 : 0; i < issued; ++i)
+            mbar_wait_for(&sm.full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, kDrainLimitNs);
 }
 
 // ------------------------------------------------------------------ launchers
