@@ -108,7 +108,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     pdl_launch_dependents();
 
+    // A warp's wait has run out; stages that the producer has issued.  (Each warp waiting
+    // for its own copies and products in every call: 32 x 8192 x 57344 106 -> 110 us, with
+    // the flag 107.)
+    __shared__ int s_gave_up, s_issued;
     if (threadIdx.x == 0) {
+        s_gave_up = 0;
         for (int i = 0; i < kLoadStages; ++i) {
             mbar_init(&full_load[i], 1 + 32);  // expect_tx + 32 cp.async arrivals
             mbar_init(&empty_load[i], 1);      // MMA commit
@@ -134,6 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     bool ok = true;
+    auto give_up = [&] {
+        s_gave_up = 1;
+        report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+    };
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -142,12 +151,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             prefetch_tmap(&tmQ);
         }
         pdl_wait();  // X' comes from the pre-pass kernel
-        int issued = 0;
-        for (int i = 0; i < nkb; ++i) {
+        int i = 0;
+        for (; i < nkb; ++i) {
             const int kb = kb_begin + i;
             const int st = i % kLoadStages;
-            const bool w = i < kLoadStages || mbar_wait(&empty_load[st], ((i / kLoadStages) - 1) & 1);
-            if (!__all_sync(0xffffffffu, w)) {
+            if (i >= kLoadStages && !mbar_wait(&empty_load[st], ((i / kLoadStages) - 1) & 1)) {
                 ok = false;
                 break;
             }
@@ -171,15 +179,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                            zero_word_src(p.zeros, g, p.N / 8, in ? wi : 0, lane), in ? 4u : 0u);
             }
             cp_async_arrive_noinc(&full_load[st]);
-            ++issued;
         }
-        if (!ok && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
-        // The copies issued land before the ring takes the pushed partials and the CTA
-        // can exit, whichever warp's wait ran out.
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if (lane == 0)
-            for (int i = issued > kLoadStages ? issued - kLoadStages : 0; i < issued; ++i)
-                mbar_wait_for(&full_load[i % kLoadStages], (i / kLoadStages) & 1, kDrainLimitNs);
+        if (lane == 0) s_issued = i;
+        if (!ok && lane == 0) give_up();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         const uint32_t idesc = tc_idesc_f16(kBN, p.nt);
@@ -206,12 +209,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
         if (lane == 0) {
-            // tmem_full completes once every MMA issued has completed; this lane
-            // waits for that itself before TMEM is freed, because a consumer's wait
-            // for it may have run out
+            // tmem_full completes once every MMA issued has completed
             tc_commit(tmem_full);
-            if (!ok) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
-            mbar_wait_for(tmem_full, 0, kDrainLimitNs);
+            if (!ok) give_up();
         }
         __syncwarp();
     } else {
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&full_a[as]);
         }
-        if (!ok && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+        if (!ok && lane == 0) give_up();
     }
 
     // ---------------------------------------------------------------- epilogue
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // laid out there as [source rank][token][owned column].
     const bool dq = warp >= 2;  // a dequantization warp
     const bool have_acc = dq && __all_sync(0xffffffffu, ok && mbar_wait(tmem_full, 0));
-    if (dq && !have_acc && lane == 0) report(p.status, AWQ_ERR_DEVICE_TIMEOUT);
+    if (dq && !have_acc && lane == 0) give_up();
     // Every CTA of the cluster is past its main loop (its load ring, which
     // receives the partials, is idle) and has initialized its barriers.
     cluster_arrive_release();
@@ -349,6 +349,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (s_gave_up) {
+        // The copies and the products issued land before tensor memory is freed and the
+        // CTA exits, whichever warp's wait ran out.
+        if (warp == 0 && lane == 0)
+            for (int i = s_issued > kLoadStages ? s_issued - kLoadStages : 0; i < s_issued; ++i)
+                mbar_wait_for(&full_load[i % kLoadStages], (i / kLoadStages) & 1, kDrainLimitNs);
+        if (warp == 1 && lane == 0) mbar_wait_for(tmem_full, 0, kDrainLimitNs);
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
