@@ -71,7 +71,10 @@ extern "C" {
                                4: every matmul takes a zero-filled workspace;
                                scale search over alpha; weight clipping;
                                5: matmul workspaces for M >= 64 hold the
-                               prefill kernel's partial tiles */
+                               prefill kernel's partial tiles.  Entry points
+                               added without a change to earlier ones (the
+                               fused epilogue, the 4-bit cache) keep it: look
+                               them up by name */
 
 typedef enum {
     AWQ_OK = 0,
