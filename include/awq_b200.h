@@ -375,7 +375,10 @@ AWQ_API awq_status_t awq_w4a16_gemm_noalloc(const uint16_t *X, const uint16_t *s
  *             (any other overlap is not allowed)
  * X, s, Q, scales, zeros, M, K, N, the workspace, the tile paths and the device
  * errors are those of awq_w4a16_gemm, and with no bias, activation, gate and
- * residual so is every bit of Y.  bias is layer state like scales; residual is
+ * residual so is every bit of Y.  As there, from 24 tokens on the dequantized
+ * weights are rounded to binary16 before they are multiplied; a gate times its
+ * column holds that error twice (3.4e-4 of the output's norm, where the output's
+ * own rounding is 2.1e-4).  bias is layer state like scales; residual is
  * read only after the previous kernel on the stream has completed.
  */
 AWQ_API awq_status_t awq_w4a16_gemm_epilogue(const uint16_t *X, const uint16_t *s, const int32_t *Q,
